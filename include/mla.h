@@ -322,6 +322,93 @@ MLA_API int mla_decode_absorbed_fp8(const mla_dims_t* dims, int32_t dtype, int32
                                     void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * The 8-bit latent cache written directly, and read back (« Cache KV, mémoire récurrente, MLA et bas
+ * rang », as above).
+ *
+ * mla_append_cache_fp8: a1 into an 8-bit cache. For each new token z, c and k_r are those of
+ *   mla_append_cache; the row stores s = max|c| / 448 in scales, E4M3(c / s) in codes (to nearest, ties to
+ *   even, saturated; s and the quotients in fp32, each rounded once; a zero row stores s = 0 and zero
+ *   codes) and k_r in the RoPE row. c is quantised from its fp32 value: it is not rounded to dtype
+ *   first, as mla_append_cache followed by mla_quantize_latent_fp8 would. The call WRITES the arrays
+ *   the descriptor names. d_c must be a multiple of 16 (else MLA_ERR_UNSUPPORTED). Other arguments,
+ *   layouts, the workspace (mla_append_workspace_size) and errors are those of mla_append_cache.
+ *   A position given twice in one call (two tokens that map to one cache row) is the caller's error:
+ *   which row is stored is then undefined.
+ * mla_read_latent_fp8: rows of the cache in storage type. Output row r, row_offsets[b] <= r <
+ *   row_offsets[b + 1], holds position p = first[b] + r - row_offsets[b] of sequence b:
+ *     out[r, 0:d_c] = s_p * value(code_p) (one rounding to dtype)     out[r, d_c:] = k_r,p
+ *   first [B] int32 (NULL: all 0)   row_offsets [B + 1] int32, from 0, not falling   out [n_rows, d_c + d_r]
+ *   dtype, row stride out_stride. Output rows from row_offsets[B] on are left as they were; offsets past
+ *   n_rows write nothing past it. A position outside the table row or a page id outside the pool is
+ *   reported (MLA_ERR_DEVICE_CHECK) and its output row left as it was. d_c a multiple of 16.
+ * ------------------------------------------------------------------------------------------- */
+MLA_API int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* x, int32_t C,
+                                 const void* w_dkv_kr, const void* gamma, const int32_t* seqlens,
+                                 const int32_t* block_table, int32_t max_pages, const mla_latent_cache_fp8_t* cache,
+                                 void* workspace, size_t ws_bytes, void* stream);
+MLA_API int mla_read_latent_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, const mla_latent_cache_fp8_t* cache,
+                                const int32_t* block_table, int32_t max_pages, const int32_t* first,
+                                const int32_t* row_offsets, int64_t n_rows, void* out, int64_t out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Attention over selected pages. The pages describe sparse attention over the latent cache only in
+ * words (« Résumé technique : GQLA … », « GQLA Sparse »); the calls below are this library's reading: blocks are
+ * the cache's 64-position pages, a page is scored by the mean of its rows, and since every head reads
+ * the same latent rows, all heads of a token attend the same pages.
+ *
+ * mla_update_page_keys (_fp8: over an 8-bit cache): for every page that holds one of the s_q newest
+ *   positions of a sequence (positions max(0, seqlens[b] - s_q) .. seqlens[b] - 1),
+ *     key_page = mean over the page's rows j below seqlens[b] of [c_j ; k_r,j]       (fp32 sums, one rounding)
+ *   keys [num_pages, d_c + d_r] dtype, one row per pool page, row stride key_stride. s_q at least the
+ *   longest sequence rebuilds every key. Other pages' keys are left as they were; a sequence of length
+ *   0 writes nothing. The 8-bit form wants d_c a multiple of 16.
+ * mla_score_pages: for each token (b, t), over the pages p that it sees (those with a position it sees),
+ *     u_h,p = sm_scale * q_abs[b,t,h,:] · key_p          scores[b,t,p] = sum_h softmax_p(u_h)_p
+ *   scores [B, s_q, max_pages] fp32; entries of pages the token does not see are left as they were. A
+ *   page id outside the pool is reported and scored as an all-zero key. num_pages: pages of the pool,
+ *   rows of keys. workspace: at least mla_score_pages_workspace_size(...) bytes (may be 0).
+ * mla_select_pages: the min(k, visible pages) pages of largest score of each token, in ascending order:
+ *   pages [B, s_q, k] int32 (indices into the sequence's block-table row, -1 after the last) and counts
+ *   [B, s_q] int32. The first n_first and the last n_recent visible pages are always among them
+ *   (n_first + n_recent <= k). Equal scores go to the lower page; a NaN ranks below every number.
+ * mla_decode_absorbed_sparse (_fp8: over an 8-bit cache, dequantised rows as in
+ *   mla_decode_absorbed_fp8): a3 + a4 over the visible positions of the listed pages only. pages
+ *   [B, s_q, k] and counts [B, s_q] as mla_select_pages writes them; a list must be strictly ascending and
+ *   name visible pages (else MLA_ERR_DEVICE_CHECK is recorded and that token's outputs are undefined);
+ *   entries from counts on are not read. A token with count 0 gets o_lat = 0 and lse = -inf.
+ *   A list of all visible pages gives mla_decode_absorbed's result. workspace: at least
+ *   mla_decode_sparse_workspace_size / mla_decode_sparse_fp8_workspace_size bytes.
+ * Errors otherwise as in the calls above.
+ * ------------------------------------------------------------------------------------------- */
+MLA_API int mla_update_page_keys(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q,
+                                 const mla_latent_cache_t* cache, const int32_t* block_table, int32_t max_pages,
+                                 const int32_t* seqlens, void* keys, int64_t key_stride, void* stream);
+MLA_API int mla_update_page_keys_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q,
+                                     const mla_latent_cache_fp8_t* cache, const int32_t* block_table, int32_t max_pages,
+                                     const int32_t* seqlens, void* keys, int64_t key_stride, void* stream);
+MLA_API size_t mla_score_pages_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q,
+                                              int32_t max_pages);
+MLA_API int mla_score_pages(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* q_abs,
+                            const void* keys, int64_t key_stride, int32_t num_pages, const int32_t* block_table,
+                            int32_t max_pages, const int32_t* seqlens, float* scores, void* workspace, size_t ws_bytes,
+                            void* stream);
+MLA_API int mla_select_pages(const mla_dims_t* dims, int32_t B, int32_t s_q, const float* scores, int32_t max_pages,
+                             const int32_t* seqlens, int32_t k, int32_t n_first, int32_t n_recent, int32_t* pages,
+                             int32_t* counts, void* stream);
+MLA_API size_t mla_decode_sparse_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, int32_t k);
+MLA_API int mla_decode_absorbed_sparse(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* q_abs,
+                                       const mla_latent_cache_t* cache, const int32_t* block_table, int32_t max_pages,
+                                       const int32_t* seqlens, const int32_t* pages, const int32_t* counts, int32_t k,
+                                       void* o_lat, float* lse, void* workspace, size_t ws_bytes, void* stream);
+MLA_API size_t mla_decode_sparse_fp8_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q,
+                                                    int32_t k);
+MLA_API int mla_decode_absorbed_sparse_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q,
+                                           const void* q_abs, const mla_latent_cache_fp8_t* cache,
+                                           const int32_t* block_table, int32_t max_pages, const int32_t* seqlens,
+                                           const int32_t* pages, const int32_t* counts, int32_t k, void* o_lat,
+                                           float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Status.
  * mla_check_status: synchronises `stream`, returns the device status word of the current device
  * (MLA_OK when no kernel recorded an error since the last call) and clears it.

@@ -81,6 +81,27 @@ SIGNATURES = {
     "mla_decode_fp8_workspace_size": (c_size_t, [PD, c_int32, c_int32, c_int32]),
     "mla_decode_absorbed_fp8": (c_int32, [PD, c_int32, c_int32, c_int32, c_void_p, POINTER(MlaLatentCacheFp8), PI,
                                           c_int32, PI, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "mla_append_cache_fp8": (c_int32, [PD, c_int32, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p, PI, PI,
+                                       c_int32, POINTER(MlaLatentCacheFp8), c_void_p, c_size_t, c_void_p]),
+    "mla_read_latent_fp8": (c_int32, [PD, c_int32, c_int32, POINTER(MlaLatentCacheFp8), PI, c_int32, PI, PI, c_int64,
+                                      c_void_p, c_int64, c_void_p]),
+    "mla_update_page_keys": (c_int32, [PD, c_int32, c_int32, c_int32, POINTER(MlaLatentCache), PI, c_int32, PI,
+                                       c_void_p, c_int64, c_void_p]),
+    "mla_update_page_keys_fp8": (c_int32, [PD, c_int32, c_int32, c_int32, POINTER(MlaLatentCacheFp8), PI, c_int32, PI,
+                                           c_void_p, c_int64, c_void_p]),
+    "mla_score_pages_workspace_size": (c_size_t, [PD, c_int32, c_int32, c_int32, c_int32]),
+    "mla_score_pages": (c_int32, [PD, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_int32, PI, c_int32, PI,
+                                  c_void_p, c_void_p, c_size_t, c_void_p]),
+    "mla_select_pages": (c_int32, [PD, c_int32, c_int32, c_void_p, c_int32, PI, c_int32, c_int32, c_int32, PI, PI,
+                                   c_void_p]),
+    "mla_decode_sparse_workspace_size": (c_size_t, [PD, c_int32, c_int32, c_int32, c_int32]),
+    "mla_decode_absorbed_sparse": (c_int32, [PD, c_int32, c_int32, c_int32, c_void_p, POINTER(MlaLatentCache), PI,
+                                             c_int32, PI, PI, PI, c_int32, c_void_p, c_void_p, c_void_p, c_size_t,
+                                             c_void_p]),
+    "mla_decode_sparse_fp8_workspace_size": (c_size_t, [PD, c_int32, c_int32, c_int32, c_int32]),
+    "mla_decode_absorbed_sparse_fp8": (c_int32, [PD, c_int32, c_int32, c_int32, c_void_p, POINTER(MlaLatentCacheFp8),
+                                                 PI, c_int32, PI, PI, PI, c_int32, c_void_p, c_void_p, c_void_p,
+                                                 c_size_t, c_void_p]),
     "mla_check_status": (c_int32, [c_void_p]),
     "mla_status_string": (c_char_p, [c_int32]),
     "mla_build_info": (c_char_p, []),

@@ -1,0 +1,177 @@
+// The 8-bit latent cache written straight from the projection, and read back into the storage type.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "simt.cuh"
+
+namespace mla {
+namespace cache8 {
+
+// Two E4M3 codes (low byte first) as fp32 values. Exact: every E4M3 value is an fp16 value.
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t pair) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Codes of four values over a scale: E4M3(v / s), to nearest, ties to even, saturated at +-448; a zero
+// magnitude is +0. `safe` is s, or 1 for a zero row.
+__device__ __forceinline__ uint32_t e4m3x4_codes(const float* v, float safe) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const float a = __fdiv_rn(v[k], safe), b = __fdiv_rn(v[k + 1], safe);
+    uint16_t pr;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pr) : "f"(b), "f"(a));   // a -> low byte
+    uint32_t lo = pr & 0xffu, hi = pr >> 8;
+    if ((lo & 0x7fu) == 0u) lo = 0u;
+    if ((hi & 0x7fu) == 0u) hi = 0u;
+    out |= (lo | (hi << 8)) << (8 * k);
+  }
+  return out;
+}
+
+// =============================================================================================
+// Append into the 8-bit cache, second half: as append_finish_kernel sums the K slices, normalises and
+// rotates, but the latent row leaves as codes and one scale. The row is quantised from its fp32 values
+// (no rounding to 16 bits in between), so the stored row is the nearest one to c itself. One block per
+// new token; d_c % 16 == 0.
+// =============================================================================================
+template <typename T>
+__global__ void append_fp8_finish_kernel(const float* __restrict__ part, int ksplit, int n_tok, int s_q, int d_c, int d_r,
+                                         const T* __restrict__ gamma, float eps, float rope_base,
+                                         const int32_t* __restrict__ seqlens, const int32_t* __restrict__ block_table,
+                                         int max_pages, uint8_t* codes, int64_t code_stride, float* scales, T* rope,
+                                         int64_t rope_stride, int num_pages, int groups) {
+  extern __shared__ float z[];
+  __shared__ float red[32];
+  __shared__ long long s_row;   // the token's cache row; -1: none (reported)
+  __shared__ int s_pos;
+  grid_dependency_wait();   // launched with programmatic dependent launch after the projection
+  allow_dependents();
+  const int N = d_c + d_r;
+  const float* cs_sn = simt::finish_gather(part, ksplit, n_tok, s_q, N, d_r, rope_base, seqlens, block_table, max_pages,
+                                           num_pages, groups, z, &s_row, &s_pos);
+  float ss = 0.f;
+  for (int i = threadIdx.x; i < d_c; i += blockDim.x) ss = fmaf(z[i], z[i], ss);
+  ss = block_sum(ss, red);
+  const float inv = 1.0f / sqrtf(ss / (float)d_c + eps);
+  const int64_t row = s_row;
+  if (row < 0) return;
+  float amax = 0.f;
+  for (int i = threadIdx.x; i < d_c; i += blockDim.x) {
+    const float v = z[i] * inv * (gamma ? ld(gamma + i) : 1.f);
+    z[i] = v;
+    amax = fmaxf(amax, fabsf(v));
+  }
+  amax = warp_max(amax);
+  __syncthreads();   // red is reused; z is complete
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  __syncthreads();
+  amax = 0.f;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, red[w]);
+  const float s = __fdiv_rn(amax, 448.f);
+  const float safe = s > 0.f ? s : 1.f;
+  uint8_t* dst = codes + row * code_stride;
+  for (int i = threadIdx.x * 4; i < d_c; i += blockDim.x * 4)
+    *reinterpret_cast<uint32_t*>(dst + i) = e4m3x4_codes(z + i, safe);
+  if (threadIdx.x == 0) scales[row] = s;
+  simt::finish_rope(z + d_c, d_r / 2, groups > 0 ? cs_sn : nullptr, s_pos, d_r, rope_base, rope + row * rope_stride);
+}
+
+// =============================================================================================
+// Read back: out row r (row_offsets[b] <= r < row_offsets[b + 1]) = [s · value(code) ; k_r] of position
+// first[b] + r - row_offsets[b] of sequence b. Bound by its bytes: d_c + 4 + d_r·e in, (d_c + d_r)·e out
+// per row. A block takes kReadRows consecutive rows: one warp finds the sequence of the first by a
+// 32-way search of row_offsets, a thread per row walks on from there and looks its cache row up, and
+// then all threads move 16 codes each at a time.
+// =============================================================================================
+constexpr int kReadRows = 64;
+constexpr int kReadThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kReadThreads)
+read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const float* __restrict__ scales,
+                const T* __restrict__ rope, int64_t rope_stride, int num_pages, const int32_t* __restrict__ block_table,
+                int max_pages, const int32_t* __restrict__ first, const int32_t* __restrict__ row_offsets, int B,
+                int64_t n_rows, int d_c, int d_r, T* __restrict__ out, int64_t out_stride) {
+  __shared__ int64_t src_row[kReadRows];   // -1: nothing to write there
+  __shared__ float src_scale[kReadRows];
+  __shared__ int s_b;
+  grid_dependency_wait();
+  allow_dependents();
+  const int64_t r0 = (int64_t)blockIdx.x * kReadRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    // the last b in [0, B] with row_offsets[b] <= r0: each step keeps the one of 32 pieces that holds it
+    int lo = 0, hi = B;
+    while (lo < hi) {
+      const int step = (hi - lo + 31) / 32;
+      const int at = lo + (lane + 1) * step;
+      const bool le = at <= hi && (int64_t)__ldg(row_offsets + at) <= r0;
+      const int n = __popc(__ballot_sync(0xffffffffu, le));   // offsets do not fall: the first n hold
+      lo += n * step;
+      hi = min(hi, lo + step - 1);
+    }
+    if (lane == 0) s_b = lo;
+  }
+  __syncthreads();
+  if (threadIdx.x < kReadRows) {
+    const int64_t r = r0 + threadIdx.x;
+    int64_t row = -1;
+    int b = s_b;
+    while (b < B && r >= (int64_t)row_offsets[b + 1]) ++b;
+    if (r < n_rows && b < B) {
+      const int64_t p = (int64_t)(first ? first[b] : 0) + (r - row_offsets[b]);
+      if (r < row_offsets[b] || p < 0 || (p >> 6) >= max_pages) report(MLA_ERR_DEVICE_CHECK);
+      else row = cache_row(block_table + (int64_t)b * max_pages, (int)p, num_pages);
+    }
+    src_row[threadIdx.x] = row;
+    src_scale[threadIdx.x] = row >= 0 ? scales[row] : 0.f;
+  }
+  __syncthreads();
+  const int pieces = d_c / 16;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < kReadRows * pieces; i += kReadThreads) {
+    const int r = i / pieces, c = i % pieces;
+    const int64_t row = src_row[r];
+    if (row < 0) continue;
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(codes + row * code_stride) + c);
+    const float sc = src_scale[r];
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+    float f[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 x = e4m3x2_values(q[k >> 1] >> (16 * (k & 1)) & 0xffffu);
+      f[2 * k] = x.x * sc;
+      f[2 * k + 1] = x.y * sc;
+    }
+    T* dst = out + (r0 + r) * out_stride + 16 * c;
+    constexpr int V = simt::Vec16<T>::n;
+#pragma unroll
+    for (int k = 0; k < 16; k += V) simt::Vec16<T>::store(dst + k, f + k);
+  }
+  // the RoPE keys are copied as stored
+  constexpr int E = 16 / (int)sizeof(T);
+  if (d_r % E == 0) {
+    const int rp = d_r / E;
+    for (int i = threadIdx.x; i < kReadRows * rp; i += kReadThreads) {
+      const int r = i / rp, c = i % rp;
+      const int64_t row = src_row[r];
+      if (row >= 0)
+        reinterpret_cast<uint4*>(out + (r0 + r) * out_stride + d_c)[c] =
+            __ldcs(reinterpret_cast<const uint4*>(rope + row * rope_stride) + c);
+    }
+  } else {
+    for (int i = threadIdx.x; i < kReadRows * d_r; i += kReadThreads) {
+      const int r = i / d_r, c = i % d_r;
+      const int64_t row = src_row[r];
+      if (row >= 0) out[(r0 + r) * out_stride + d_c + c] = rope[row * rope_stride + c];
+    }
+  }
+}
+
+}  // namespace cache8
+}  // namespace mla

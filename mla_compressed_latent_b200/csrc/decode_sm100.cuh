@@ -131,18 +131,33 @@ struct Params {
   // 1: launched without any merge because the host's copy of seqlens cut no sequence; a cut found
   // here from the device's seqlens is then reported (its parts would stay unmerged)
   int expect_whole;
+  // page-selecting decode only: row v (= b * list_s_q + t) attends the pages page_list[v * list_k + i],
+  // i < counts[v], of its sequence; then B counts the rows v, s_q is 1 and max_tiles is list_k
+  const int32_t* page_list;
+  const int32_t* counts;
+  int list_k, list_s_q;
 };
 
 // ---- work split -----------------------------------------------------------------------------------
 __host__ __device__ __forceinline__ int tiles_of(int L, int max_tiles) { return L > 0 ? min((L + kTile - 1) / kTile, max_tiles) : 0; }
 
+// Tiles of work item b. Dense: the pages of sequence b, from its length. Sparse: the pages listed for row
+// b (`lens` is then the array of counts).
+template <bool kSparse>
+__device__ __forceinline__ int item_tiles(const int32_t* __restrict__ lens, int b, int max_tiles) {
+  const int L = __ldg(lens + b);
+  if constexpr (kSparse) return min(max(L, 0), max_tiles);
+  else return tiles_of(L, max_tiles);
+}
+
 // Walks the segments (sequence, tile range) of one pair's contiguous range of the global tile list.
+template <bool kSparse>
 struct SegIter {
   long long cur, end, off_b;
   int b;
-  __device__ bool next(const int32_t* seqlens, int B, int max_tiles, int& bo, int& t_lo, int& t_hi, int& tiles_b) {
+  __device__ bool next(const int32_t* lens, int B, int max_tiles, int& bo, int& t_lo, int& t_hi, int& tiles_b) {
     while (cur < end && b < B) {
-      const int tb = tiles_of(seqlens[b], max_tiles);
+      const int tb = item_tiles<kSparse>(lens, b, max_tiles);
       if (cur >= off_b + tb) {
         off_b += tb;
         ++b;
@@ -174,16 +189,17 @@ __host__ __device__ __forceinline__ bool whole_sequences(int B, int npairs, long
 
 // One warp: total tiles T, this pair's range, and the sequence holding its first tile. Lane l scans
 // sequences [l*per, (l+1)*per).
-__device__ void plan_range(const int32_t* seqlens, int B, int s_q, int max_tiles, int pair, int npairs, long long* out) {
+template <bool kSparse>
+__device__ void plan_range(const int32_t* lens, int B, int s_q, int max_tiles, int pair, int npairs, long long* out) {
   const int lane = threadIdx.x & 31;
   const int per = (B + 31) / 32;
   const int b0 = min(B, lane * per), b1 = min(B, b0 + per);
   long long local = 0;
   int max_tb = 0;
   for (int b = b0; b < b1; ++b) {
-    const int L = seqlens[b];
-    if (L < s_q || (L + kTile - 1) / kTile > max_tiles) report(MLA_ERR_DEVICE_CHECK);
-    const int tb = tiles_of(L, max_tiles);
+    const int L = lens[b];
+    if (kSparse ? (L < 0 || L > max_tiles) : (L < s_q || (L + kTile - 1) / kTile > max_tiles)) report(MLA_ERR_DEVICE_CHECK);
+    const int tb = item_tiles<kSparse>(lens, b, max_tiles);
     local += tb;
     max_tb = max(max_tb, tb);
   }
@@ -208,8 +224,8 @@ __device__ void plan_range(const int32_t* seqlens, int B, int s_q, int max_tiles
       if (lane == 0) { out[0] = 0; out[1] = 0; out[2] = 0; out[3] = B; }
     } else if (grp >= b0 && grp < b1) {
       long long off = excl;
-      for (int b = b0; b < grp; ++b) off += tiles_of(seqlens[b], max_tiles);
-      out[0] = off; out[1] = off + tiles_of(seqlens[grp], max_tiles); out[2] = off; out[3] = grp;
+      for (int b = b0; b < grp; ++b) off += item_tiles<kSparse>(lens, b, max_tiles);
+      out[0] = off; out[1] = off + item_tiles<kSparse>(lens, grp, max_tiles); out[2] = off; out[3] = grp;
     }
     return;
   }
@@ -218,7 +234,7 @@ __device__ void plan_range(const int32_t* seqlens, int B, int s_q, int max_tiles
   if (start < end && start >= excl && start < incl) {
     long long off = excl;
     for (int b = b0; b < b1; ++b) {
-      const int tb = tiles_of(seqlens[b], max_tiles);
+      const int tb = item_tiles<kSparse>(lens, b, max_tiles);
       if (start < off + tb) {
         out[0] = start; out[1] = end; out[2] = off; out[3] = b;
         break;
@@ -236,17 +252,18 @@ __device__ __forceinline__ int pair_of(long long x, long long T, int P) { return
 // One warp combines the parts of new token v (= b * s_q + tok) and head h, if its sequence was cut:
 // the parts come from pair (group, tok) of the groups that covered the sequence's tiles. T = total
 // tiles, G = groups; lane l holds sequences [b0, b1) for the prefix of tiles before b.
-__device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ seqlens, int s_q, int max_tiles, int G,
+template <bool kSparse>
+__device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ lens, int s_q, int max_tiles, int G,
                                                  long long T, int b0, int b1, int v, int h,
                                                  const float* __restrict__ part_o, const float* __restrict__ part_lse,
                                                  __nv_bfloat16* __restrict__ o_lat, float* __restrict__ lse) {
   const int lane = threadIdx.x & 31;
   const int b = v / s_q, tok = v % s_q;
   long long before = 0;
-  for (int x = b0; x < min(b1, b); ++x) before += tiles_of(__ldg(seqlens + x), max_tiles);
+  for (int x = b0; x < min(b1, b); ++x) before += item_tiles<kSparse>(lens, x, max_tiles);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  const long long off = before, tb = tiles_of(__ldg(seqlens + b), max_tiles);
+  const long long off = before, tb = item_tiles<kSparse>(lens, b, max_tiles);
   if (tb == 0) return;
   const int p0 = pair_of(off, T, G), p1 = pair_of(off + tb - 1, T, G);   // groups
   if (p0 == p1) return;                       // written whole by one group
@@ -346,6 +363,7 @@ __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, uin
 // Output CTA: 0 TMA producer | 1 O-MMA issuer | 2 TMEM, then receiver (returns the score CTA's
 // staging buffers as tiles land) | 4-11 row warps: rescale of their own rows of O when a running
 // maximum moved, and the epilogue.
+template <bool kSparse>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
               const __grid_constant__ CUtensorMap tm_q, const Params p) {
@@ -390,14 +408,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
   }
   // nothing above touched global memory; from here on the previous kernel's results are needed
   grid_dependency_wait();
-  if (warp == 3) plan_range(p.seqlens, p.B, p.s_q, p.max_tiles, pair, npairs, work);
+  // what an item's tile count is read from: sequence lengths, or the number of pages a row lists
+  const int32_t* lens = kSparse ? p.counts : p.seqlens;
+  if (warp == 3) plan_range<kSparse>(lens, p.B, p.s_q, p.max_tiles, pair, npairs, work);
   ptx::tc_fence_before();
   __syncthreads();
   // (allow_dependents() only at the end: the merge that follows would park its blocks on these SMs)
   ptx::cluster_sync();      // the peer's barriers are initialised before any remote arrive
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + kOffTmemSlot);
-  SegIter segs{work[0], work[1], work[2], (int)work[3]};
+  SegIter<kSparse> segs{work[0], work[1], work[2], (int)work[3]};
   int b, t_lo, t_hi, tiles_b;
   // row-warp geometry (warps 4-11)
   const int qd = warp & 3, sub = (warp - 4) >> 2;
@@ -408,7 +428,31 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
   // first seqlens[b] - s_q + 1 + tok positions of its sequence
   const int tok = pair % p.s_q;
   auto vrow = [&](int bb) -> long long { return (long long)bb * p.s_q + tok; };
-  auto vlen = [&](int bb) -> int { return p.seqlens[bb] - (p.s_q - 1 - tok); };
+  // positions of the item's tiles laid end to end that it sees (sparse: every listed page but the last
+  // is full; the last one ends where the token's visible positions end)
+  auto vlen = [&](int bb) -> int {
+    if constexpr (kSparse) {
+      const int n = item_tiles<true>(lens, bb, p.max_tiles);
+      if (n == 0) return 0;
+      const int vis = p.seqlens[bb / p.list_s_q] - (p.list_s_q - 1 - bb % p.list_s_q);
+      const long long left = (long long)vis - (long long)p.page_list[(long long)bb * p.list_k + n - 1] * kTile;
+      return (n - 1) * kTile + (int)min(max(left, 0ll), (long long)kTile);
+    } else {
+      return p.seqlens[bb] - (p.s_q - 1 - tok);
+    }
+  };
+  // pool page of the item's tile t; -1 when the list names no visible page there or is not ascending
+  auto page_at = [&](int bb, int t) -> int {
+    if constexpr (kSparse) {
+      const int32_t* list = p.page_list + (long long)bb * p.list_k;
+      const int seq = bb / p.list_s_q, pg = list[t], before = t > 0 ? list[t - 1] : -1;
+      const int vis = p.seqlens[seq] - (p.list_s_q - 1 - bb % p.list_s_q);
+      if (pg <= before || pg >= p.max_pages || pg > (vis - 1) / kTile || vis <= 0) return -1;
+      return p.block_table[(long long)seq * p.max_pages + pg];
+    } else {
+      return p.block_table[(long long)bb * p.max_pages + t];
+    }
+  };
 
   if (rank == 0) {
     // ============================== score CTA ==============================
@@ -417,7 +461,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
         uint32_t it = 0;
         bool ok = true;
         uint32_t gi = 0;
-        while (ok && segs.next(p.seqlens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+        while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
           // the sequence's absorbed query first: box (column block cb, head half rh)
           for (int qg = 0; qg < kQGroups && ok; ++qg, ++gi) {
             const uint32_t s = gi % kRing;
@@ -429,7 +473,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
             }
           }
           for (int t = t_lo; t < t_hi && ok; ++t, ++it) {
-            int page = p.block_table[(long long)b * p.max_pages + t];   // issued before the wait
+            int page = page_at(b, t);   // issued before the wait
             for (int q = 0; q < kGroupsPerTile && ok; ++q, ++gi) {
               const uint32_t s = gi % kRing;
               if (!(ok = wait_bar(bar(K_EMPTY + s), ((gi / kRing) & 1u) ^ 1u, abort_addr, false))) break;
@@ -454,7 +498,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
         const uint32_t slot_remote0 = ptx::map_to_cta(base + kOffPSlots, 1);
         uint32_t it = 0;
         bool ok = true;
-        while (ok && segs.next(p.seqlens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+        while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
           for (int t = t_lo; t < t_hi; ++t, ++it) {
             const uint32_t stg = it % kStaging, slot = it % kPSlots;
             if (!(ok = wait_bar(bar(P_WRITTEN + stg), (it / kStaging) & 1u, abort_addr, false))) break;
@@ -479,7 +523,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       const uint64_t k_desc = ptx::smem_desc_sw128(base + kOffK, 16, 1024);
       uint32_t it = 0, seg = 0, gq = 0;
       bool ok = true;
-      while (ok && segs.next(p.seqlens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+      while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
         if (!(ok = wait_bar_warp(bar(Q_FULL), seg & 1u, abort_addr, false))) break;
         if (parity == 0 && lane == 0)   // every row-warp thread has copied its part of the query out of the ring
           for (int qg = 0; qg < kQGroups; ++qg) ptx::mbar_arrive(bar(K_EMPTY + (gq + qg) % kRing));
@@ -528,7 +572,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       float* dec = reinterpret_cast<float*>(gbase + kOffStats);   // [128]: m after the latest tile
       uint32_t it = 0, seg = 0, gq = 0;
       bool ok = true;
-      while (ok && segs.next(p.seqlens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+      while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
         const int L = vlen(b);
         // Q̃ of this sequence into TMEM columns [0, 288), from the 6 ring groups that carry it (every
         // S MMA of the previous segment is done: the row warps met after its last result). Set g
@@ -560,9 +604,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
         }
         int nb = -1;
         {
-          SegIter peek = segs;
+          SegIter<kSparse> peek = segs;
           int x0, x1, x2;
-          if (!peek.next(p.seqlens, p.B, p.max_tiles, nb, x0, x1, x2)) nb = -1;
+          if (!peek.next(lens, p.B, p.max_tiles, nb, x0, x1, x2)) nb = -1;
         }
         gq += kGroupsPerTile * (t_hi - t_lo);
         float m_own = -INFINITY, l_own = 0.f;   // this set's running maximum and partial row sum
@@ -685,7 +729,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       if (lane == 0) {   // ---- receiver: as each tile lands, the score CTA may reuse that staging buffer
         uint32_t it = 0;
         bool ok = true;
-        while (ok && segs.next(p.seqlens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+        while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
           for (int t = t_lo; t < t_hi; ++t, ++it) {
             if (!(ok = wait_bar(bar(P_FULL + it % kPSlots), (it / kPSlots) & 1u, abort_addr, true))) break;
             ptx::mbar_arrive_remote(bar(STG_FREE + it % kStaging), 0);
@@ -696,10 +740,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       if (lane == 0) {   // ---- TMA producer: latent rows c of each tile
         uint32_t it = 0;
         bool ok = true;
-        while (ok && segs.next(p.seqlens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+        while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
           for (int t = t_lo; t < t_hi && ok; ++t, ++it) {
             const uint32_t s = it % kVStages;
-            int page = p.block_table[(long long)b * p.max_pages + t];   // issued before the wait
+            int page = page_at(b, t);   // issued before the wait
             if (!(ok = wait_bar(bar(V_EMPTY + s), ((it / kVStages) & 1u) ^ 1u, abort_addr, false))) break;
             if (page < 0 || page >= p.num_pages) page = p.num_pages;   // reported by the score CTA
             const uint32_t dst = base + kOffV + s * kVStageBytes;
@@ -710,6 +754,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
         for (uint32_t k = (it > (uint32_t)kVStages ? it - kVStages : 0); k < it; ++k)
           wait_bar(bar(V_FULL + k % kVStages), (k / kVStages) & 1u, abort_addr, false, false);
       }
+    } else if (kSparse && warp == 3) {
+      // ---- rows that list no page attend nothing: zeros and lse = -inf (they have no tiles, so no
+      // pair works on them)
+      for (int v = pair; v < p.B; v += npairs) {
+        if (item_tiles<kSparse>(lens, v, p.max_tiles) > 0) continue;
+        uint4* o = reinterpret_cast<uint4*>(p.o_lat + (size_t)v * kH * kDC);
+        for (int i = lane; i < kH * kDC / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = lane; i < kH; i += 32) p.lse[(size_t)v * kH + i] = -INFINITY;
+      }
     } else if (warp == 1) {
       // ---- MMA issuer (an elected lane) with the warp's help for masking: O += P · C, K = 64 positions in
       // 4 steps of 16, N = 512 in 2 halves. A tile's P is complete (and O rescaled for it) once the
@@ -718,7 +771,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       const uint64_t p_desc0 = ptx::smem_desc_sw128(base + kOffPSlots, 16, 1024);
       uint32_t it = 0;
       bool ok = true;
-      while (ok && segs.next(p.seqlens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+      while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
         const int L = vlen(b);
         for (int t = t_lo; t < t_hi; ++t, ++it) {
           const uint32_t slot = it % kPSlots, s = it % kVStages;
@@ -772,7 +825,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       float* stats = reinterpret_cast<float*>(gbase + kOffStats);
       uint32_t it = 0, seg = 0;
       bool ok = true;
-      while (segs.next(p.seqlens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+      while (segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
         for (int t = t_lo; t < t_hi; ++t, ++it) {
           if (!ok) continue;   // after a failure: skip to the segment end, where all row warps meet
           const uint32_t slot = it % kPSlots;
@@ -900,7 +953,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       const int warps = kThreads / 32;
       const long long units = (long long)p.B * p.s_q * kH;
       for (long long u = (long long)blockIdx.x * warps + warp; u < units; u += (long long)gridDim.x * warps)
-        merge_token_head(p.seqlens, p.s_q, p.max_tiles, npairs / p.s_q, work[4], b0, b1, (int)(u / kH), (int)(u % kH),
+        merge_token_head<kSparse>(lens, p.s_q, p.max_tiles, npairs / p.s_q, work[4], b0, b1, (int)(u / kH), (int)(u % kH),
                          p.part_o, p.part_lse, p.o_lat, p.lse);
     }
     allow_dependents();
@@ -912,8 +965,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
 // partial loads before combining them.
 constexpr int kMergeHeads = 4;
 constexpr int kMergeTokenBlocks = 8;   // blocks along the tokens; each strides over them
+template <bool kSparse>
 __global__ void __launch_bounds__(32 * kMergeHeads)
-merge_kernel(const int32_t* __restrict__ seqlens, int B, int s_q, int max_tiles, int npairs, const float* __restrict__ part_o,
+merge_kernel(const int32_t* __restrict__ lens, int B, int s_q, int max_tiles, int npairs, const float* __restrict__ part_o,
              const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ o_lat, float* __restrict__ lse) {
   // blocks stride over the new tokens v = b * s_q + tok; a token's parts come from pair (group, tok) of
   // the groups that covered its sequence's tiles
@@ -928,7 +982,7 @@ merge_kernel(const int32_t* __restrict__ seqlens, int B, int s_q, int max_tiles,
   long long local = 0;
   int max_tb = 0;
   for (int x = b0; x < b1; ++x) {
-    const int tb = tiles_of(__ldg(seqlens + x), max_tiles);
+    const int tb = item_tiles<kSparse>(lens, x, max_tiles);
     local += tb;
     max_tb = max(max_tb, tb);
   }
@@ -940,7 +994,7 @@ merge_kernel(const int32_t* __restrict__ seqlens, int B, int s_q, int max_tiles,
   const long long T = local;
   if (T == 0 || G == 0 || whole_sequences(B, G, T, max_tb)) return;   // nothing was cut
   for (int v = blockIdx.x; v < B * s_q; v += gridDim.x)
-    merge_token_head(seqlens, s_q, max_tiles, G, T, b0, b1, v, blockIdx.y * kMergeHeads + warp, part_o, part_lse, o_lat, lse);
+    merge_token_head<kSparse>(lens, s_q, max_tiles, G, T, b0, b1, v, blockIdx.y * kMergeHeads + warp, part_o, part_lse, o_lat, lse);
 }
 
 // ---- host side -----------------------------------------------------------------------------------------
@@ -963,6 +1017,7 @@ inline bool make_tmap(CUtensorMap* m, const void* base, int64_t cols, int64_t ro
   return tmap::make_bf16_sw128(m, base, cols, rows, stride_elems, kTile);
 }
 
+template <bool kSparse>
 inline int active_pairs(int num_sms) {
   static int cached[64] = {0};
   int dev = 0;
@@ -974,7 +1029,7 @@ inline int active_pairs(int num_sms) {
   cfg.gridDim = dim3(2 * max_pairs(num_sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
-  if (cudaOccupancyMaxActiveClusters(&n, decode_kernel, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, decode_kernel<kSparse>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = max_pairs(num_sms);
   }
@@ -988,15 +1043,26 @@ inline int active_pairs(int num_sms) {
 inline bool g_test_two_launches = false;
 #endif
 
+// The page lists of the sparse decode (page_list null: the dense decode).
+struct PageLists {
+  const int32_t* pages = nullptr;    // [rows, k]
+  const int32_t* counts = nullptr;   // [rows]
+  int k = 0;
+  int s_q = 1;                       // rows (tokens) per sequence of the block table and seqlens
+};
+
+// Dense: B sequences with s_q new tokens each. Sparse: B rows (tokens), s_q = 1.
+template <bool kSparse>
 inline int launch_decode(const mla_dims_t* d, int32_t B, int32_t s_q, const void* q_abs, const mla_latent_cache_t* cache,
                          const int32_t* block_table, int32_t max_pages, const int32_t* seqlens, void* o_lat, float* lse,
-                         void* workspace, size_t ws_bytes, int num_sms, const int32_t* seqlens_host, cudaStream_t st) {
+                         void* workspace, size_t ws_bytes, int num_sms, const int32_t* seqlens_host, cudaStream_t st,
+                         const PageLists& lists = PageLists()) {
   if (!workspace || ws_bytes < decode_workspace_bytes(d, MLA_BF16, B, s_q, num_sms)) return MLA_ERR_WORKSPACE;
   static bool attr_done[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_done[dev]) {
-    if (cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(decode_kernel<kSparse>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
       return MLA_ERR_CUDA;
     attr_done[dev] = true;
   }
@@ -1006,7 +1072,7 @@ inline int launch_decode(const mla_dims_t* d, int32_t B, int32_t s_q, const void
   if (!make_tmap(&tm_rope, cache->rope, kDR, rows, cache->rope_stride)) return MLA_ERR_INVALID_ARG;
   CUtensorMap tm_q;   // q_abs as [B*s_q*128 heads, 576]: boxes of 64 heads x 64 columns
   if (!make_tmap(&tm_q, q_abs, kRow, (int64_t)B * s_q * kH, kRow)) return MLA_ERR_INVALID_ARG;
-  const int P = active_pairs(num_sms);
+  const int P = active_pairs<kSparse>(num_sms);
   if (P < s_q) return MLA_ERR_UNSUPPORTED;   // every token of a sequence needs a pair of its own
   Params prm;
   prm.q_abs = reinterpret_cast<const __nv_bfloat16*>(q_abs);
@@ -1016,7 +1082,11 @@ inline int launch_decode(const mla_dims_t* d, int32_t B, int32_t s_q, const void
   prm.seqlens = seqlens;
   prm.B = B;
   prm.s_q = s_q;
-  prm.max_tiles = max_pages;
+  prm.max_tiles = kSparse ? lists.k : max_pages;
+  prm.page_list = lists.pages;
+  prm.counts = lists.counts;
+  prm.list_k = lists.k;
+  prm.list_s_q = lists.s_q;
   prm.o_lat = reinterpret_cast<__nv_bfloat16*>(o_lat);
   prm.lse = lse;
   prm.part_o = reinterpret_cast<float*>(workspace);
@@ -1036,7 +1106,7 @@ inline int launch_decode(const mla_dims_t* d, int32_t B, int32_t s_q, const void
     if (T == 0 || whole_sequences(B, P / s_q, T, max_tb)) {
       prm.merge_in_kernel = 0;
       prm.expect_whole = 1;
-      launch_pdl(decode_kernel, dim3(2 * P), dim3(kThreads), kSmemBytes, st, tm_lat, tm_rope, tm_q, prm);
+      launch_pdl(decode_kernel<kSparse>, dim3(2 * P), dim3(kThreads), kSmemBytes, st, tm_lat, tm_rope, tm_q, prm);
       return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
     }
   }
@@ -1053,9 +1123,9 @@ inline int launch_decode(const mla_dims_t* d, int32_t B, int32_t s_q, const void
   for (int mode = forced ? 3 : (coop_mode[di] ? coop_mode[di] : 1); mode <= 3; ++mode) {
     if (mode == 3) {
       prm.merge_in_kernel = 0;
-      launch_pdl(decode_kernel, dim3(2 * P), dim3(kThreads), kSmemBytes, st, tm_lat, tm_rope, tm_q, prm);
-      launch_pdl(merge_kernel, dim3(std::min(B * s_q, kMergeTokenBlocks), kH / kMergeHeads), dim3(32 * kMergeHeads), 0,
-                 st, seqlens, (int)B, (int)s_q, (int)max_pages, P, (const float*)prm.part_o,
+      launch_pdl(decode_kernel<kSparse>, dim3(2 * P), dim3(kThreads), kSmemBytes, st, tm_lat, tm_rope, tm_q, prm);
+      launch_pdl(merge_kernel<kSparse>, dim3(std::min(B * s_q, kMergeTokenBlocks), kH / kMergeHeads),
+                 dim3(32 * kMergeHeads), 0, st, kSparse ? lists.counts : seqlens, (int)B, (int)s_q, prm.max_tiles, P, (const float*)prm.part_o,
                  (const float*)prm.part_lse, prm.o_lat, lse);
       if (!forced) coop_mode[di] = 3;
       break;
@@ -1073,7 +1143,7 @@ inline int launch_decode(const mla_dims_t* d, int32_t B, int32_t s_q, const void
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = mode == 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, decode_kernel, tm_lat, tm_rope, tm_q, prm) == cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, decode_kernel<kSparse>, tm_lat, tm_rope, tm_q, prm) == cudaSuccess) {
       g_launches.fetch_add(1, std::memory_order_relaxed);
       coop_mode[di] = mode;
       break;

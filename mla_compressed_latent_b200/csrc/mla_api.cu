@@ -15,6 +15,8 @@
 #include "decode_sm100.cuh"
 #include "gemm_sm100.cuh"
 #include "gqla_sm100.cuh"
+#include "cache8.cuh"
+#include "pages.cuh"
 
 namespace {
 
@@ -171,6 +173,31 @@ int launch_decode_simt(DecodeArgs A, int n_tok, void* ws, size_t ws_bytes, cudaS
   return launch_status();
 }
 
+template <typename T, bool kCodes>
+int launch_page_keys(const mla_dims_t* dims, int32_t B, int32_t s_q, const mla::pages::CacheView<T>& view,
+                     const int32_t* block_table, int32_t max_pages, const int32_t* seqlens, void* keys,
+                     int64_t key_stride, cudaStream_t st) {
+  const int W = dims->d_c + dims->d_r;
+  // pages that s_q consecutive positions can touch, at most a whole table row
+  const int per_seq = (int)std::min<int64_t>(max_pages, ((int64_t)s_q + 62) / 64 + 1);
+  if ((int64_t)B * per_seq > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  const size_t smem = (size_t)mla::pages::kKeyGroups * W * sizeof(float);
+  constexpr int V = mla::simt::Vec16<T>::n;
+  auto go = [&](auto kernel, int v) -> int {
+    if (int rc = set_smem(kernel, smem)) return rc;
+    const int threads = std::min(mla::pages::kKeyThreads, (W / v * mla::pages::kKeyGroups + 31) / 32 * 32);
+    mla::launch_pdl(kernel, dim3(B * per_seq), dim3(threads), smem, st, view, block_table, max_pages, seqlens, s_q,
+                    per_seq, dims->d_c, dims->d_r, (T*)keys, key_stride);
+    return launch_status();
+  };
+  if constexpr (kCodes) {
+    if (dims->d_c % 16 || dims->d_r % V) return MLA_ERR_UNSUPPORTED;
+    return go(mla::pages::page_keys_kernel<T, V, true>, V);
+  } else {
+    if (dims->d_c % V == 0 && dims->d_r % V == 0) return go(mla::pages::page_keys_kernel<T, V, false>, V);
+    return go(mla::pages::page_keys_kernel<T, 1, false>, 1);
+  }
+}
 }  // namespace
 
 extern "C" {
@@ -518,7 +545,7 @@ int mla_decode_absorbed_hinted(const mla_dims_t* dims, int32_t dtype, int32_t B,
 
   if (mla::sm100::decode_supported(dims, dtype, B, s_q)) {
     const mla_dims_t dd = with_scale(dims);
-    return mla::sm100::launch_decode(&dd, B, s_q, q_abs, cache, block_table, max_pages, seqlens, o_lat, lse,
+    return mla::sm100::launch_decode<false>(&dd, B, s_q, q_abs, cache, block_table, max_pages, seqlens, o_lat, lse,
                                      workspace, ws_bytes, num_sms(), seqlens_host, st);
   }
 
@@ -636,7 +663,7 @@ int mla_decode_absorbed_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, in
     if ((rc = launch_status())) return rc;
     mla_latent_cache_t dense{ws + f.lat, dims->d_c, ws + f.rope, dims->d_r, B * max_pages};
     const mla_dims_t dd = with_scale(dims);
-    return mla::sm100::launch_decode(&dd, B, s_q, q_abs, &dense, (const int32_t*)(ws + f.table), max_pages, seqlens,
+    return mla::sm100::launch_decode<false>(&dd, B, s_q, q_abs, &dense, (const int32_t*)(ws + f.table), max_pages, seqlens,
                                      o_lat, lse, ws + f.dec, ws_bytes - f.dec, num_sms(), nullptr, st);
   }
   if (dims->H % mla::simt::DEC_HEADS || dims->d_c % 32 || dims->d_c > 32 * mla::simt::DEC_MAX_OV)
@@ -658,6 +685,301 @@ int mla_decode_absorbed_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, in
   A.nsplit = sp.nsplit; A.chunk = sp.chunk;
   return dtype == MLA_F32 ? launch_decode_simt<float>(A, n_tok, workspace, ws_bytes, st)
                           : launch_decode_simt<__nv_bfloat16>(A, n_tok, workspace, ws_bytes, st);
+}
+
+// ------------------------------------------------------------------------------------------------
+// 8-bit cache: append and read back
+// ------------------------------------------------------------------------------------------------
+namespace {
+// The descriptor of an 8-bit cache; MLA_OK or the error status.
+int fp8_cache_args(const mla_dims_t* dims, int32_t dtype, const mla_latent_cache_fp8_t* cache) {
+  if (!cache || !cache->codes || !cache->scales || !cache->rope || cache->num_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(cache->codes) || !aligned16(cache->scales) || !aligned16(cache->rope)) return MLA_ERR_INVALID_ARG;
+  if (cache->code_stride < dims->d_c || cache->code_stride % 16 || !stride_ok(cache->rope_stride, dtype, dims->d_r))
+    return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+int latent_cache_args(const mla_dims_t* dims, int32_t dtype, const mla_latent_cache_t* cache) {
+  if (!cache || !cache->latent || !cache->rope || cache->num_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(cache->latent) || !aligned16(cache->rope)) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(cache->latent_stride, dtype, dims->d_c) || !stride_ok(cache->rope_stride, dtype, dims->d_r))
+    return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+}  // namespace
+
+int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* x, int32_t C,
+                         const void* w_dkv_kr, const void* gamma, const int32_t* seqlens, const int32_t* block_table,
+                         int32_t max_pages, const mla_latent_cache_fp8_t* cache, void* workspace, size_t ws_bytes,
+                         void* stream) {
+  int rc = check_dims(dims);
+  if (rc) return rc;
+  if ((rc = check_dtype(dtype))) return rc;
+  if (!tokens_ok(B, s_q) || C <= 0 || max_pages <= 0 || !x || !w_dkv_kr || !seqlens || !block_table)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_dkv_kr) || (gamma && !aligned16(gamma)) || !aligned16(seqlens) ||
+      !aligned16(block_table))
+    return MLA_ERR_INVALID_ARG;
+  if ((rc = fp8_cache_args(dims, dtype, cache))) return rc;
+  if (dims->d_c % 16) return MLA_ERR_UNSUPPORTED;
+  const int n_tok = B * s_q, N = dims->d_c + dims->d_r;
+  const bool tc = append_on_tc(dtype, C, N);
+  const int ks = tc ? append_tc_splits(n_tok, C, N) : append_ksplit(n_tok, C, N);
+  if (!workspace || ws_bytes < (size_t)ks * n_tok * N * sizeof(float)) return MLA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const FinishShape fs = finish_shape(N, dims->d_r, workspace);
+  // attributes first: a failure here leaves nothing enqueued
+  if ((rc = dtype == MLA_F32 ? set_smem(mla::cache8::append_fp8_finish_kernel<float>, fs.smem)
+                             : set_smem(mla::cache8::append_fp8_finish_kernel<__nv_bfloat16>, fs.smem)))
+    return rc;
+  float* part = reinterpret_cast<float*>(workspace);
+  auto run = [&](auto zero) -> int {
+    using T = decltype(zero);
+    if (tc) {
+      mla::gemm::Params p{};
+      p.mode = 1;
+      p.part = part;
+      p.w_early = 1;
+      if (int e = mla::gemm::run(with_sms({w_dkv_kr, x, 1, C, N, n_tok, ks}), p, st)) return e;
+    } else {
+      const int k_chunk = ((C + ks - 1) / ks + 63) / 64 * 64;
+      dim3 grid((N + mla::simt::PROJ_COLS - 1) / mla::simt::PROJ_COLS,
+                (n_tok + mla::simt::PROJ_TOK - 1) / mla::simt::PROJ_TOK, ks);
+      launch(mla::simt::proj_partial_kernel<T>, grid, mla::simt::PROJ_COLS, 0, st, (const T*)x, n_tok, C,
+             (const T*)w_dkv_kr, N, k_chunk, part, (T*)nullptr);
+    }
+    mla::launch_pdl(mla::cache8::append_fp8_finish_kernel<T>, dim3(n_tok), dim3(fs.threads), fs.smem, st,
+                    (const float*)part, ks, n_tok, s_q, dims->d_c, dims->d_r, (const T*)gamma, dims->rms_eps,
+                    dims->rope_base, seqlens, block_table, max_pages, const_cast<uint8_t*>(cache->codes),
+                    cache->code_stride, const_cast<float*>(cache->scales), (T*)const_cast<void*>(cache->rope),
+                    cache->rope_stride, cache->num_pages, fs.groups);
+    return launch_status();
+  };
+  return dtype == MLA_F32 ? run(0.f) : run(__nv_bfloat16());
+}
+
+int mla_read_latent_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, const mla_latent_cache_fp8_t* cache,
+                        const int32_t* block_table, int32_t max_pages, const int32_t* first, const int32_t* row_offsets,
+                        int64_t n_rows, void* out, int64_t out_stride, void* stream) {
+  int rc = check_dims(dims);
+  if (rc) return rc;
+  if ((rc = check_dtype(dtype))) return rc;
+  if (B <= 0 || max_pages <= 0 || n_rows <= 0 || !block_table || !row_offsets || !out) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(block_table) || (first && !aligned16(first)) || !aligned16(row_offsets) || !aligned16(out))
+    return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(out_stride, dtype, (int64_t)dims->d_c + dims->d_r)) return MLA_ERR_INVALID_ARG;
+  if ((rc = fp8_cache_args(dims, dtype, cache))) return rc;
+  if (dims->d_c % 16) return MLA_ERR_UNSUPPORTED;
+  const int64_t blocks = (n_rows + mla::cache8::kReadRows - 1) / mla::cache8::kReadRows;
+  if (blocks > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto run = [&](auto zero) -> int {
+    using T = decltype(zero);
+    mla::launch_pdl(mla::cache8::read_fp8_kernel<T>, dim3((unsigned)blocks), dim3(mla::cache8::kReadThreads), 0, st,
+                    (const uint8_t*)cache->codes, cache->code_stride, (const float*)cache->scales,
+                    (const T*)cache->rope, cache->rope_stride, cache->num_pages, block_table, max_pages, first,
+                    row_offsets, B, n_rows, dims->d_c, dims->d_r, (T*)out, out_stride);
+    return launch_status();
+  };
+  return dtype == MLA_F32 ? run(0.f) : run(__nv_bfloat16());
+}
+
+// ------------------------------------------------------------------------------------------------
+// Page keys, scores and selection
+// ------------------------------------------------------------------------------------------------
+namespace {
+int page_keys_args(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const int32_t* block_table,
+                   int32_t max_pages, const int32_t* seqlens, const void* keys, int64_t key_stride) {
+  int rc = check_dims(dims);
+  if (rc) return rc;
+  if ((rc = check_dtype(dtype))) return rc;
+  if (B <= 0 || s_q <= 0 || max_pages <= 0 || !block_table || !seqlens || !keys) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(block_table) || !aligned16(seqlens) || !aligned16(keys)) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(key_stride, dtype, (int64_t)dims->d_c + dims->d_r)) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+}  // namespace
+
+int mla_update_page_keys(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const mla_latent_cache_t* cache,
+                         const int32_t* block_table, int32_t max_pages, const int32_t* seqlens, void* keys,
+                         int64_t key_stride, void* stream) {
+  int rc = page_keys_args(dims, dtype, B, s_q, block_table, max_pages, seqlens, keys, key_stride);
+  if (rc || (rc = latent_cache_args(dims, dtype, cache))) return rc;
+  auto run = [&](auto zero) -> int {
+    using T = decltype(zero);
+    const mla::pages::CacheView<T> view{(const T*)cache->latent, cache->latent_stride, nullptr, 0, nullptr,
+                                        (const T*)cache->rope, cache->rope_stride, cache->num_pages};
+    return launch_page_keys<T, false>(dims, B, s_q, view, block_table, max_pages, seqlens, keys, key_stride,
+                                      reinterpret_cast<cudaStream_t>(stream));
+  };
+  return dtype == MLA_F32 ? run(0.f) : run(__nv_bfloat16());
+}
+
+int mla_update_page_keys_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q,
+                             const mla_latent_cache_fp8_t* cache, const int32_t* block_table, int32_t max_pages,
+                             const int32_t* seqlens, void* keys, int64_t key_stride, void* stream) {
+  int rc = page_keys_args(dims, dtype, B, s_q, block_table, max_pages, seqlens, keys, key_stride);
+  if (rc || (rc = fp8_cache_args(dims, dtype, cache))) return rc;
+  auto run = [&](auto zero) -> int {
+    using T = decltype(zero);
+    const mla::pages::CacheView<T> view{nullptr, 0, cache->codes, cache->code_stride, cache->scales,
+                                        (const T*)cache->rope, cache->rope_stride, cache->num_pages};
+    return launch_page_keys<T, true>(dims, B, s_q, view, block_table, max_pages, seqlens, keys, key_stride,
+                                     reinterpret_cast<cudaStream_t>(stream));
+  };
+  return dtype == MLA_F32 ? run(0.f) : run(__nv_bfloat16());
+}
+
+size_t mla_score_pages_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, int32_t max_pages) {
+  if (check_dims(dims) || check_dtype(dtype) || !tokens_ok(B, s_q) || max_pages <= 0) return 0;
+  return (size_t)B * s_q * dims->H * ((size_t)max_pages + 1) * sizeof(float);
+}
+
+int mla_score_pages(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* q_abs, const void* keys,
+                    int64_t key_stride, int32_t num_pages, const int32_t* block_table, int32_t max_pages,
+                    const int32_t* seqlens, float* scores, void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_dims(dims);
+  if (rc) return rc;
+  if ((rc = check_dtype(dtype))) return rc;
+  if (!tokens_ok(B, s_q) || max_pages <= 0 || num_pages <= 0 || !q_abs || !keys || !block_table || !seqlens || !scores)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_abs) || !aligned16(keys) || !aligned16(block_table) || !aligned16(seqlens) || !aligned16(scores) ||
+      (workspace && !aligned16(workspace)))
+    return MLA_ERR_INVALID_ARG;
+  const int W = dims->d_c + dims->d_r, H = dims->H, n_tok = B * s_q;
+  if (!stride_ok(key_stride, dtype, W)) return MLA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  using namespace mla::pages;
+  if (!workspace || ws_bytes < mla_score_pages_workspace_size(dims, dtype, B, s_q, max_pages)) return MLA_ERR_WORKSPACE;
+  const int64_t page_tiles = ((int64_t)max_pages + kScorePages - 1) / kScorePages;
+  if (page_tiles > 65535 || (H + kScoreHeads - 1) / kScoreHeads > 65535 || (int64_t)n_tok * H > INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
+  ScoreArgs A{block_table, max_pages, num_pages, seqlens, s_q, H, W, score_scale(dims), nullptr, nullptr, scores};
+  A.u = reinterpret_cast<float*>(workspace);
+  A.lse = A.u + (size_t)n_tok * H * max_pages;
+  const size_t smem = ((size_t)kScoreHeads * W + (size_t)kScorePages * (W + 1)) * sizeof(float);
+  auto run = [&](auto zero) -> int {
+    using T = decltype(zero);
+    if (int e = set_smem(score_products_kernel<T>, smem)) return e;
+    launch(score_products_kernel<T>, dim3(n_tok, (unsigned)page_tiles, (H + kScoreHeads - 1) / kScoreHeads),
+           32 * kScoreHeads, smem, st, A, (const T*)q_abs, (const T*)keys, key_stride);
+    launch(score_lse_kernel, n_tok * H, 256, 0, st, A);
+    launch(score_mass_kernel, dim3(n_tok, std::min((max_pages + 255) / 256, 64)), 256, 0, st, A);
+    return launch_status();
+  };
+  return dtype == MLA_F32 ? run(0.f) : run(__nv_bfloat16());
+}
+
+int mla_select_pages(const mla_dims_t* dims, int32_t B, int32_t s_q, const float* scores, int32_t max_pages,
+                     const int32_t* seqlens, int32_t k, int32_t n_first, int32_t n_recent, int32_t* pages,
+                     int32_t* counts, void* stream) {
+  int rc = check_dims(dims);
+  if (rc) return rc;
+  if (!tokens_ok(B, s_q) || max_pages <= 0 || k <= 0 || n_first < 0 || n_recent < 0 ||
+      (int64_t)n_first + n_recent > k || !scores || !seqlens || !pages || !counts)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(scores) || !aligned16(seqlens) || !aligned16(pages) || !aligned16(counts)) return MLA_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // one block per token; 2048 ranks fit a 256-thread block's registers
+  if (max_pages <= 256 * mla::pages::kKeep)
+    mla::launch_pdl(mla::pages::select_pages_kernel<256>, dim3(B * s_q), dim3(256), 0, st, scores, max_pages, seqlens, s_q,
+                    k, n_first, n_recent, pages, counts);
+  else
+    mla::launch_pdl(mla::pages::select_pages_kernel<1024>, dim3(B * s_q), dim3(1024), 0, st, scores, max_pages, seqlens,
+                    s_q, k, n_first, n_recent, pages, counts);
+  return launch_status();
+}
+
+// ------------------------------------------------------------------------------------------------
+// Decode over selected pages
+// ------------------------------------------------------------------------------------------------
+namespace {
+// The arguments both caches share; MLA_OK or the error status.
+int sparse_args(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* q_abs,
+                const int32_t* block_table, int32_t max_pages, const int32_t* seqlens, const int32_t* pages,
+                const int32_t* counts, int32_t k, const void* o_lat, const float* lse, const void* workspace) {
+  int rc = check_dims(dims);
+  if (rc) return rc;
+  if ((rc = check_dtype(dtype))) return rc;
+  if (!tokens_ok(B, s_q) || max_pages <= 0 || k <= 0 || k > INT32_MAX / 64 || !q_abs || !block_table || !seqlens || !pages ||
+      !counts || !o_lat || !lse)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_abs) || !aligned16(block_table) || !aligned16(seqlens) || !aligned16(pages) || !aligned16(counts) ||
+      !aligned16(o_lat) || !aligned16(lse) || (workspace && !aligned16(workspace)))
+    return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+int sparse_simt(const mla_dims_t* dims, int32_t dtype, DecodeArgs A, int32_t B, int32_t s_q, const void* q_abs,
+                const int32_t* block_table, int32_t max_pages, const int32_t* seqlens, const int32_t* pages,
+                const int32_t* counts, int32_t k, void* o_lat, float* lse, void* workspace, size_t ws_bytes,
+                cudaStream_t st) {
+  if (dims->H % mla::simt::DEC_HEADS || dims->d_c % 32 || dims->d_c > 32 * mla::simt::DEC_MAX_OV)
+    return MLA_ERR_UNSUPPORTED;
+  const int n_tok = B * s_q;
+  A.q = q_abs;
+  A.q_head_stride = dims->d_c + dims->d_r;
+  A.Dk = dims->d_c; A.Dv = dims->d_c; A.d_r = dims->d_r; A.H = dims->H; A.heads_per_group = dims->H;
+  A.kv_shared = 1;
+  A.block_table = block_table; A.max_pages = max_pages;
+  A.seqlens = seqlens; A.s_q = s_q; A.sm_scale = score_scale(dims); A.rope_base = dims->rope_base;
+  A.out = o_lat; A.out_head_stride = dims->d_c; A.lse = lse;
+  A.page_list = pages; A.counts = counts; A.list_k = k;
+  SimtSplit sp = simt_split(n_tok, dims->H, k);
+  A.nsplit = sp.nsplit; A.chunk = sp.chunk;
+  return dtype == MLA_F32 ? launch_decode_simt<float>(A, n_tok, workspace, ws_bytes, st)
+                          : launch_decode_simt<__nv_bfloat16>(A, n_tok, workspace, ws_bytes, st);
+}
+}  // namespace
+
+size_t mla_decode_sparse_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, int32_t k) {
+  if (check_dims(dims) || check_dtype(dtype) || !tokens_ok(B, s_q) || k <= 0) return 0;
+  if (mla::sm100::decode_supported(dims, dtype, B * s_q, 1))
+    return mla::sm100::decode_workspace_bytes(dims, dtype, B * s_q, 1, num_sms());
+  return simt_decode_ws(B * s_q, dims->H, dims->d_c, k);
+}
+
+int mla_decode_absorbed_sparse(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* q_abs,
+                               const mla_latent_cache_t* cache, const int32_t* block_table, int32_t max_pages,
+                               const int32_t* seqlens, const int32_t* pages, const int32_t* counts, int32_t k,
+                               void* o_lat, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  int rc = sparse_args(dims, dtype, B, s_q, q_abs, block_table, max_pages, seqlens, pages, counts, k, o_lat, lse,
+                       workspace);
+  if (rc || (rc = latent_cache_args(dims, dtype, cache))) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (mla::sm100::decode_supported(dims, dtype, B * s_q, 1)) {
+    const mla_dims_t dd = with_scale(dims);
+    return mla::sm100::launch_decode<true>(&dd, B * s_q, 1, q_abs, cache, block_table, max_pages, seqlens, o_lat, lse,
+                                           workspace, ws_bytes, num_sms(), nullptr, st, {pages, counts, k, s_q});
+  }
+  DecodeArgs A{};
+  A.kpart = cache->latent; A.k_stride = cache->latent_stride;
+  A.vpart = cache->latent; A.v_stride = cache->latent_stride;
+  A.rope = cache->rope; A.rope_stride = cache->rope_stride;
+  A.num_pages = cache->num_pages;
+  return sparse_simt(dims, dtype, A, B, s_q, q_abs, block_table, max_pages, seqlens, pages, counts, k, o_lat, lse,
+                     workspace, ws_bytes, st);
+}
+
+size_t mla_decode_sparse_fp8_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, int32_t k) {
+  if (check_dims(dims) || check_dtype(dtype) || !tokens_ok(B, s_q) || k <= 0) return 0;
+  return simt_decode_ws(B * s_q, dims->H, dims->d_c, k);
+}
+
+int mla_decode_absorbed_sparse_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* q_abs,
+                                   const mla_latent_cache_fp8_t* cache, const int32_t* block_table, int32_t max_pages,
+                                   const int32_t* seqlens, const int32_t* pages, const int32_t* counts, int32_t k,
+                                   void* o_lat, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  int rc = sparse_args(dims, dtype, B, s_q, q_abs, block_table, max_pages, seqlens, pages, counts, k, o_lat, lse,
+                       workspace);
+  if (rc || (rc = fp8_cache_args(dims, dtype, cache))) return rc;
+  DecodeArgs A{};
+  A.kpart = cache->codes; A.k_stride = cache->code_stride; A.kscale = cache->scales;
+  A.vpart = cache->codes; A.v_stride = cache->code_stride;
+  A.rope = cache->rope; A.rope_stride = cache->rope_stride;
+  A.num_pages = cache->num_pages;
+  return sparse_simt(dims, dtype, A, B, s_q, q_abs, block_table, max_pages, seqlens, pages, counts, k, o_lat, lse,
+                     workspace, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------------------------------------

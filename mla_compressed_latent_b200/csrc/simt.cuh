@@ -106,23 +106,17 @@ template <> struct Vec16<__nv_bfloat16> {
 // threads of the slice readers in the groups > 0 layout (the place-finding warp follows them)
 __host__ __device__ inline int finish_readers(int N, int groups) { return (groups * (N / 4) + 31) / 32 * 32; }
 
-template <typename T>
-__global__ void append_finish_kernel(const float* __restrict__ part, int ksplit, int n_tok, int s_q,
-                                     int d_c, int d_r, const T* __restrict__ gamma, float eps,
-                                     float rope_base, const int32_t* __restrict__ seqlens,
-                                     const int32_t* __restrict__ block_table, int max_pages,
-                                     T* latent, int64_t lat_stride, T* rope, int64_t rope_stride,
-                                     int num_pages, int latent_by_token, int groups) {
-  extern __shared__ float z[];
-  __shared__ float red[32];
-  __shared__ long long s_row;   // the token's cache row; -1: none (reported)
-  __shared__ int s_pos;
-  grid_dependency_wait();   // launched with programmatic dependent launch after the projection
-  allow_dependents();
+// First half of an append finish, for token blockIdx.x: z[0..N) = the sums over the K slices (shared
+// memory), its cache row (-1: none, reported) and position in *s_row and *s_pos, and with groups > 0
+// the rotation's cos, sin of pair i at [2i], [2i + 1] of the array it returns.
+__device__ __forceinline__ float* finish_gather(const float* __restrict__ part, int ksplit, int n_tok, int s_q, int N,
+                                                int d_r, float rope_base, const int32_t* __restrict__ seqlens,
+                                                const int32_t* __restrict__ block_table, int max_pages,
+                                                int num_pages, int groups, float* z, long long* s_row, int* s_pos) {
   const int tok = blockIdx.x;
   const int b = tok / s_q, t = tok % s_q;
-  const int N = d_c + d_r, half = d_r / 2;
-  float* cs_sn = z + (1 + groups) * N;   // groups > 0: cos, sin of pair i at [2i], [2i + 1]
+  const int half = d_r / 2;
+  float* cs_sn = z + (1 + groups) * N;
   if (groups > 0) {
     const int Q = N / 4, readers = finish_readers(N, groups);
     float* acc = z + N;   // [groups][N]
@@ -135,8 +129,8 @@ __global__ void append_finish_kernel(const float* __restrict__ part, int ksplit,
         pos = seqlens[b] - s_q + t;
         if (pos < 0 || (pos >> 6) >= max_pages) report(MLA_ERR_DEVICE_CHECK);
         else row = cache_row(block_table + (int64_t)b * max_pages, pos, num_pages);
-        s_row = row;
-        s_pos = pos;
+        *s_row = row;
+        *s_pos = pos;
       }
       pos = __shfl_sync(0xffffffffu, pos, 0);
       for (int i = lane; i < half; i += 32) rope_cos_sin(pos, i, d_r, rope_base, &cs_sn[2 * i], &cs_sn[2 * i + 1]);
@@ -172,11 +166,49 @@ __global__ void append_finish_kernel(const float* __restrict__ part, int ksplit,
       const int pos = seqlens[b] - s_q + t;
       if (pos < 0 || (pos >> 6) >= max_pages) report(MLA_ERR_DEVICE_CHECK);
       else row = cache_row(block_table + (int64_t)b * max_pages, pos, num_pages);
-      s_row = row;
-      s_pos = pos;
+      *s_row = row;
+      *s_pos = pos;
     }
   }
   __syncthreads();
+  return cs_sn;
+}
+
+// The rotated key of one token from its projected values zr [d_r]; cs_sn: ready cos/sin pairs, or null.
+template <typename T>
+__device__ __forceinline__ void finish_rope(const float* zr, int half, const float* cs_sn, int pos, int d_r,
+                                            float rope_base, T* dst) {
+  for (int i = threadIdx.x; i < half; i += blockDim.x) {
+    float cs, sn;
+    if (cs_sn) {
+      cs = cs_sn[2 * i];
+      sn = cs_sn[2 * i + 1];
+    } else {
+      rope_cos_sin(pos, i, d_r, rope_base, &cs, &sn);
+    }
+    const float a = zr[2 * i], bb = zr[2 * i + 1];
+    st(dst + 2 * i, a * cs - bb * sn);
+    st(dst + 2 * i + 1, a * sn + bb * cs);
+  }
+}
+
+template <typename T>
+__global__ void append_finish_kernel(const float* __restrict__ part, int ksplit, int n_tok, int s_q,
+                                     int d_c, int d_r, const T* __restrict__ gamma, float eps,
+                                     float rope_base, const int32_t* __restrict__ seqlens,
+                                     const int32_t* __restrict__ block_table, int max_pages,
+                                     T* latent, int64_t lat_stride, T* rope, int64_t rope_stride,
+                                     int num_pages, int latent_by_token, int groups) {
+  extern __shared__ float z[];
+  __shared__ float red[32];
+  __shared__ long long s_row;   // the token's cache row; -1: none (reported)
+  __shared__ int s_pos;
+  grid_dependency_wait();   // launched with programmatic dependent launch after the projection
+  allow_dependents();
+  const int tok = blockIdx.x;
+  const int N = d_c + d_r, half = d_r / 2;
+  const float* cs_sn = finish_gather(part, ksplit, n_tok, s_q, N, d_r, rope_base, seqlens, block_table, max_pages, num_pages,
+                                     groups, z, &s_row, &s_pos);
   float ss = 0.f;
   for (int i = threadIdx.x; i < d_c; i += blockDim.x) ss = fmaf(z[i], z[i], ss);
   ss = block_sum(ss, red);
@@ -196,18 +228,7 @@ __global__ void append_finish_kernel(const float* __restrict__ part, int ksplit,
   } else {
     for (int i = threadIdx.x; i < d_c; i += blockDim.x) st(lrow + i, z[i] * inv * (gamma ? ld(gamma + i) : 1.f));
   }
-  for (int i = threadIdx.x; i < half; i += blockDim.x) {
-    float cs, sn;
-    if (groups > 0) {
-      cs = cs_sn[2 * i];
-      sn = cs_sn[2 * i + 1];
-    } else {
-      rope_cos_sin(pos, i, d_r, rope_base, &cs, &sn);
-    }
-    const float a = z[d_c + 2 * i], bb = z[d_c + 2 * i + 1];
-    st(rope + row * rope_stride + 2 * i, a * cs - bb * sn);
-    st(rope + row * rope_stride + 2 * i + 1, a * sn + bb * cs);
-  }
+  finish_rope(z + d_c, half, groups > 0 ? cs_sn : nullptr, pos, d_r, rope_base, rope + row * rope_stride);
 }
 
 // =============================================================================================
@@ -411,6 +432,9 @@ struct DecodeArgs {
   float sm_scale, rope_base;
   void* out; int64_t out_head_stride; float* lse;
   float* part_o; float* part_lse; int nsplit; int chunk;
+  // page-selecting decode: token tok attends pages page_list[tok * list_k + i], i < counts[tok], laid
+  // end to end (nullptr: every visible position)
+  const int32_t* page_list; const int32_t* counts; int list_k;
 };
 
 // Value of an E4M3 code from the format's definition: sign, exponent field e (bias 7), mantissa m;
@@ -503,11 +527,16 @@ decode_simt_kernel(DecodeArgs A) {
   const int h = h0 + warp;
   const int grp = h0 / A.heads_per_group;      // all 8 heads of a block share one group
   const int L = A.seqlens[b];
-  const int n_vis = L - A.s_q + t + 1;
+  const int vis = L - A.s_q + t + 1;
+  const int32_t* list = A.page_list ? A.page_list + (int64_t)tok * A.list_k : nullptr;
+  // positions to walk: the visible ones, or the listed pages' slots laid end to end
+  const int n_vis = list ? 64 * min(max(A.counts[tok], 0), A.list_k) : vis;
   const int lo = split * A.chunk;
   const int hi = min(n_vis, lo + A.chunk);
   const int32_t* table = A.block_table + (int64_t)b * A.max_pages;
-  if (n_vis < 1 || (L > 0 && ((L - 1) >> 6) >= A.max_pages)) {
+  if (list) {
+    if (threadIdx.x == 0 && (A.counts[tok] < 0 || A.counts[tok] > A.list_k)) report(MLA_ERR_DEVICE_CHECK);
+  } else if (n_vis < 1 || (L > 0 && ((L - 1) >> 6) >= A.max_pages)) {
     if (threadIdx.x == 0 && split == 0 && blockIdx.y == 0) report(MLA_ERR_DEVICE_CHECK);
     return;
   }
@@ -541,8 +570,19 @@ decode_simt_kernel(DecodeArgs A) {
   for (int p0 = lo; p0 < hi; p0 += DEC_TILE) {
     __syncthreads();
     if (threadIdx.x < DEC_TILE) {
-      const int p = p0 + threadIdx.x;
-      const int64_t row = (p < hi) ? cache_row(table, p, A.num_pages) : -1;
+      int p = p0 + threadIdx.x;
+      int64_t row = -1;
+      if (p < hi && list) {
+        const int i = p >> 6, pg = list[i], before = i > 0 ? list[i - 1] : -1;
+        if (pg <= before || pg >= A.max_pages || (int64_t)pg * 64 >= vis) {
+          report(MLA_ERR_DEVICE_CHECK);
+        } else {
+          p = pg * 64 + (p & 63);
+          if (p < vis) row = cache_row(table, p, A.num_pages);
+        }
+      } else if (p < hi) {
+        row = cache_row(table, p, A.num_pages);
+      }
       rows[threadIdx.x] = row;
       if (fp8) rscale[threadIdx.x] = row >= 0 ? A.kscale[row] : 0.f;
     }
@@ -654,7 +694,7 @@ __global__ void merge_splits_kernel(const float* __restrict__ part_o, const floa
   for (int s = 0; s < nsplit; ++s) m = fmaxf(m, pl[s]);
   float tot = 0.f;
   for (int s = 0; s < nsplit; ++s) tot += (pl[s] == -INFINITY) ? 0.f : expf(pl[s] - m);
-  const float inv = 1.f / tot;
+  const float inv = tot > 0.f ? 1.f / tot : 0.f;   // no visible position at all: zeros and lse = -inf
   for (int d = threadIdx.x; d < Dv; d += blockDim.x) {
     float acc = 0.f;
     for (int s = 0; s < nsplit; ++s) {

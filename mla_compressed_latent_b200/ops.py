@@ -276,6 +276,227 @@ def mla_decode_absorbed_fp8(dims: Dims, q_abs, cache: LatentCacheFp8, block_tabl
     return o_lat, lse
 
 
+# ---- 8-bit cache written directly and read back; attention over selected pages -----------------
+# These calls check what they are given: a tensor of another shape or dtype, one that is not contiguous
+# where the library wants rows laid end to end, or one that is not on the current device raises before
+# anything is enqueued.
+def _current(t: torch.Tensor) -> int:
+    """The current device, which has to hold t (the library enqueues on it)."""
+    if not t.is_cuda:
+        raise ValueError(f"libmla takes device tensors, got {t.device}")
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"libmla takes tensors of the current device (cuda:{dev}), got {t.device}")
+    return dev
+
+
+def _need(dev: int, name: str, t: torch.Tensor, shape, dtype) -> int:
+    """data_ptr of a contiguous tensor of this shape and dtype on device `dev`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name}: libmla takes tensors of the current device (cuda:{dev}), got {t.device}")
+    return t.data_ptr()
+
+
+def _need_rows(dev: int, name: str, t: torch.Tensor, rows: int, width: int, dtype) -> None:
+    """A matrix of at least `rows` rows of `width` values laid end to end (rows may be strided)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected at least {rows} rows of {width} values, got {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name}: libmla takes tensors of the current device (cuda:{dev}), got {t.device}")
+
+
+def _cache_arg(dev: int, dims: Dims, cache, dtype):
+    """The checked descriptor of a latent cache (LatentCache or LatentCacheFp8)."""
+    rows = cache.num_pages * 64
+    _need_rows(dev, "cache.rope", cache.rope, rows, dims.d_r, dtype)
+    if isinstance(cache, LatentCacheFp8):
+        _need_rows(dev, "cache.codes", cache.codes, rows, dims.d_c, torch.uint8)
+        if cache.scales.dim() != 1 or cache.scales.shape[0] < rows:
+            raise ValueError(f"cache.scales: expected at least {rows} values, got {tuple(cache.scales.shape)}")
+        _need(dev, "cache.scales", cache.scales, cache.scales.shape, torch.float32)
+    else:
+        _need_rows(dev, "cache.latent", cache.latent, rows, dims.d_c, dtype)
+    return cache.c()
+
+
+def _table(dev: int, B: int, block_table, seqlens):
+    """(block table, its row length, lengths) as pointers and sizes."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [B, max_pages]")
+    max_pages = block_table.shape[1]
+    return (_need(dev, "block_table", block_table, (B, max_pages), torch.int32), max_pages,
+            None if seqlens is None else _need(dev, "seqlens", seqlens, (B,), torch.int32))
+
+
+def _space(dev: int, nbytes: int, workspace):
+    """(workspace or None, its pointer, its size): taken from torch's allocator when none is given."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _stream_on(dev: int, stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device_index != dev:
+        raise ValueError(f"stream: expected a stream of the current device (cuda:{dev})")
+    return stream.cuda_stream
+
+
+def _width(dims: Dims) -> int:
+    return dims.d_c + dims.d_r
+
+
+def mla_append_cache_fp8(dims: Dims, x, w_dkv_kr, gamma, seqlens, block_table, cache: LatentCacheFp8, workspace=None,
+                         stream=None):
+    """a1 into an 8-bit cache: the new tokens' latents leave the projection as E4M3 codes and one scale
+    per row (quantised from fp32), their RoPE keys as in mla_append_cache. x [B, s_q, C], w_dkv_kr
+    [C, d_c + d_r], gamma [d_c] or None."""
+    lib = L.load()
+    dt = _dt(x)
+    B, s_q, C = x.shape
+    dev = _current(x)
+    px = _need(dev, "x", x, (B, s_q, C), x.dtype)
+    pw = _need(dev, "w_dkv_kr", w_dkv_kr, (C, _width(dims)), x.dtype)
+    pg = None if gamma is None else _need(dev, "gamma", gamma, (dims.d_c,), x.dtype)
+    table, max_pages, lens = _table(dev, B, block_table, seqlens)
+    cc = _cache_arg(dev, dims, cache, x.dtype)
+    d = dims.c()
+    need = lib.mla_append_workspace_size(ctypes.byref(d), B, s_q, C)
+    workspace, ws, wsb = _space(dev, need, workspace)
+    rc = lib.mla_append_cache_fp8(ctypes.byref(d), dt, B, s_q, px, C, pw, pg, lens, table, max_pages, ctypes.byref(cc),
+                                  ws, wsb, _stream_on(dev, stream))
+    _check("mla_append_cache_fp8", rc)
+
+
+def mla_read_latent_fp8(dims: Dims, cache: LatentCacheFp8, block_table, row_offsets, out, first=None, stream=None):
+    """Rows of an 8-bit cache back in storage type: out[row_offsets[b] + i] = [c ; k_r] of position
+    first[b] + i (first None: from position 0) of sequence b. out [n_rows, d_c + d_r]; rows from
+    row_offsets[B] on are left as they were."""
+    lib = L.load()
+    dt = _dt(out)
+    dev = _current(out)
+    B = block_table.shape[0]
+    table, max_pages, _ = _table(dev, B, block_table, None)
+    off = _need(dev, "row_offsets", row_offsets, (B + 1,), torch.int32)
+    pf = None if first is None else _need(dev, "first", first, (B,), torch.int32)
+    _need_rows(dev, "out", out, 1, _width(dims), out.dtype)
+    cc = _cache_arg(dev, dims, cache, out.dtype)
+    d = dims.c()
+    rc = lib.mla_read_latent_fp8(ctypes.byref(d), dt, B, ctypes.byref(cc), table, max_pages, pf, off, out.shape[0],
+                                 out.data_ptr(), out.stride(0), _stream_on(dev, stream))
+    _check("mla_read_latent_fp8", rc)
+    return out
+
+
+def mla_update_page_keys(dims: Dims, cache, block_table, seqlens, s_q: int, keys, stream=None):
+    """keys [num_pages, d_c + d_r]: the mean row of every page that holds one of a sequence's s_q newest
+    positions, from a LatentCache or a LatentCacheFp8. s_q >= the longest sequence rebuilds every key."""
+    lib = L.load()
+    dt = _dt(keys)
+    dev = _current(keys)
+    B = block_table.shape[0]
+    table, max_pages, lens = _table(dev, B, block_table, seqlens)
+    _need_rows(dev, "keys", keys, cache.num_pages, _width(dims), keys.dtype)
+    cc = _cache_arg(dev, dims, cache, keys.dtype)
+    name = "mla_update_page_keys_fp8" if isinstance(cache, LatentCacheFp8) else "mla_update_page_keys"
+    d = dims.c()
+    rc = getattr(lib, name)(ctypes.byref(d), dt, B, s_q, ctypes.byref(cc), table, max_pages, lens, keys.data_ptr(),
+                            keys.stride(0), _stream_on(dev, stream))
+    _check(name, rc)
+    return keys
+
+
+def mla_score_pages(dims: Dims, q_abs, keys, block_table, seqlens, scores=None, workspace=None, stream=None):
+    """scores [B, s_q, max_pages] (fp32): for every page a token sees, the sum over the heads of the softmax
+    over its pages of sm_scale * q_abs · key. Entries of pages it does not see are left as they were
+    (zeros in a tensor made here)."""
+    lib = L.load()
+    dt = _dt(q_abs)
+    dev = _current(q_abs)
+    B, s_q = q_abs.shape[0], q_abs.shape[1]
+    pq = _need(dev, "q_abs", q_abs, (B, s_q, dims.H, _width(dims)), q_abs.dtype)
+    table, max_pages, lens = _table(dev, B, block_table, seqlens)
+    _need_rows(dev, "keys", keys, 1, _width(dims), q_abs.dtype)
+    if scores is None:
+        scores = torch.zeros(B, s_q, max_pages, dtype=torch.float32, device=q_abs.device)
+    ps = _need(dev, "scores", scores, (B, s_q, max_pages), torch.float32)
+    d = dims.c()
+    need = lib.mla_score_pages_workspace_size(ctypes.byref(d), dt, B, s_q, max_pages)
+    workspace, ws, wsb = _space(dev, need, workspace)
+    rc = lib.mla_score_pages(ctypes.byref(d), dt, B, s_q, pq, keys.data_ptr(), keys.stride(0), keys.shape[0], table,
+                             max_pages, lens, ps, ws, wsb, _stream_on(dev, stream))
+    _check("mla_score_pages", rc)
+    return scores
+
+
+def mla_select_pages(dims: Dims, scores, seqlens, k: int, n_first: int = 0, n_recent: int = 1, pages=None, counts=None,
+                     stream=None):
+    """The k pages of largest score of each token, ascending: (pages [B, s_q, k] int32 with -1 after the
+    last, counts [B, s_q] int32). The first n_first and last n_recent visible pages are always kept."""
+    lib = L.load()
+    dev = _current(scores)
+    if scores.dim() != 3:
+        raise ValueError("scores: expected [B, s_q, max_pages]")
+    B, s_q, max_pages = scores.shape
+    ps = _need(dev, "scores", scores, (B, s_q, max_pages), torch.float32)
+    lens = _need(dev, "seqlens", seqlens, (B,), torch.int32)
+    if pages is None:
+        pages = torch.empty(B, s_q, k, dtype=torch.int32, device=scores.device)
+    if counts is None:
+        counts = torch.empty(B, s_q, dtype=torch.int32, device=scores.device)
+    pp = _need(dev, "pages", pages, (B, s_q, k), torch.int32)
+    pc = _need(dev, "counts", counts, (B, s_q), torch.int32)
+    d = dims.c()
+    rc = lib.mla_select_pages(ctypes.byref(d), B, s_q, ps, max_pages, lens, k, n_first, n_recent, pp, pc,
+                              _stream_on(dev, stream))
+    _check("mla_select_pages", rc)
+    return pages, counts
+
+
+def mla_decode_absorbed_sparse(dims: Dims, q_abs, cache, block_table, seqlens, pages, counts, o_lat=None, lse=None,
+                               workspace=None, stream=None):
+    """Absorbed decode over the visible positions of the listed pages (pages [B, s_q, k], counts [B, s_q] as
+    mla_select_pages gives them) of a LatentCache or a LatentCacheFp8. A token with no page gets zeros
+    and lse = -inf."""
+    lib = L.load()
+    dt = _dt(q_abs)
+    dev = _current(q_abs)
+    B, s_q = q_abs.shape[0], q_abs.shape[1]
+    pq = _need(dev, "q_abs", q_abs, (B, s_q, dims.H, _width(dims)), q_abs.dtype)
+    table, max_pages, lens = _table(dev, B, block_table, seqlens)
+    k = pages.shape[-1]
+    pp = _need(dev, "pages", pages, (B, s_q, k), torch.int32)
+    pc = _need(dev, "counts", counts, (B, s_q), torch.int32)
+    cc = _cache_arg(dev, dims, cache, q_abs.dtype)
+    if o_lat is None:
+        o_lat = torch.empty(B, s_q, dims.H, dims.d_c, dtype=q_abs.dtype, device=q_abs.device)
+    if lse is None:
+        lse = torch.empty(B, s_q, dims.H, dtype=torch.float32, device=q_abs.device)
+    po = _need(dev, "o_lat", o_lat, (B, s_q, dims.H, dims.d_c), q_abs.dtype)
+    pl = _need(dev, "lse", lse, (B, s_q, dims.H), torch.float32)
+    fp8 = isinstance(cache, LatentCacheFp8)
+    name = "mla_decode_absorbed_sparse_fp8" if fp8 else "mla_decode_absorbed_sparse"
+    size = lib.mla_decode_sparse_fp8_workspace_size if fp8 else lib.mla_decode_sparse_workspace_size
+    d = dims.c()
+    workspace, ws, wsb = _space(dev, size(ctypes.byref(d), dt, B, s_q, k), workspace)
+    rc = getattr(lib, name)(ctypes.byref(d), dt, B, s_q, pq, ctypes.byref(cc), table, max_pages, lens, pp, pc, k, po, pl,
+                            ws, wsb, _stream_on(dev, stream))
+    _check(name, rc)
+    return o_lat, lse
+
+
 def mla_out_proj(dims: Dims, o_lat, w_uv, out=None, w_o=None, out_model=None, stream=None):
     lib = L.load()
     B, s_q, H, _ = o_lat.shape
