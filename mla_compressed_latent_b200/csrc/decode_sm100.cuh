@@ -187,6 +187,19 @@ __host__ __device__ __forceinline__ bool whole_sequences(int B, int npairs, long
   return B <= npairs && (long long)max_tb <= (T + npairs - 1) / npairs + kSplitSlack;
 }
 
+// Groups of pairs the tiles are cut over. Sparse rows list few pages: a pair that gets less than
+// kSparseMinTiles tiles spends more on loading the query and on the merge of its part than on the tiles.
+constexpr int kSparseMinTiles = 2;
+template <bool kSparse>
+__host__ __device__ __forceinline__ int active_groups(int G, long long T) {
+  if constexpr (kSparse) {
+    const long long most = (T + kSparseMinTiles - 1) / kSparseMinTiles;
+    return most < G ? (most > 1 ? (int)most : 1) : G;
+  } else {
+    return G;
+  }
+}
+
 // One warp: total tiles T, this pair's range, and the sequence holding its first tile. Lane l scans
 // sequences [l*per, (l+1)*per).
 template <bool kSparse>
@@ -212,7 +225,7 @@ __device__ void plan_range(const int32_t* lens, int B, int s_q, int max_tiles, i
   }
   const long long T = __shfl_sync(0xffffffffu, incl, 31);
   const long long excl = incl - local;
-  const int G = npairs / s_q, grp = pair / s_q;
+  const int G = active_groups<kSparse>(npairs / s_q, T), grp = pair / s_q;
   if (lane == 0) { out[4] = T; out[5] = (G > 0 && whole_sequences(B, G, T, max_tb)) ? 1 : 0; }
   if (grp >= G) {   // left over when s_q does not divide the pairs: no work
     if (lane == 0) { out[0] = 0; out[1] = 0; out[2] = 0; out[3] = B; }
@@ -252,7 +265,6 @@ __device__ __forceinline__ int pair_of(long long x, long long T, int P) { return
 // One warp combines the parts of new token v (= b * s_q + tok) and head h, if its sequence was cut:
 // the parts come from pair (group, tok) of the groups that covered the sequence's tiles. T = total
 // tiles, G = groups; lane l holds sequences [b0, b1) for the prefix of tiles before b.
-template <bool kSparse>
 __device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ lens, int s_q, int max_tiles, int G,
                                                  long long T, int b0, int b1, int v, int h,
                                                  const float* __restrict__ part_o, const float* __restrict__ part_lse,
@@ -260,10 +272,10 @@ __device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ len
   const int lane = threadIdx.x & 31;
   const int b = v / s_q, tok = v % s_q;
   long long before = 0;
-  for (int x = b0; x < min(b1, b); ++x) before += item_tiles<kSparse>(lens, x, max_tiles);
+  for (int x = b0; x < min(b1, b); ++x) before += item_tiles<false>(lens, x, max_tiles);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  const long long off = before, tb = item_tiles<kSparse>(lens, b, max_tiles);
+  const long long off = before, tb = item_tiles<false>(lens, b, max_tiles);
   if (tb == 0) return;
   const int p0 = pair_of(off, T, G), p1 = pair_of(off + tb - 1, T, G);   // groups
   if (p0 == p1) return;                       // written whole by one group
@@ -312,6 +324,81 @@ __device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ len
     dst[32 * k] = make_uint2(ptx::pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
                              ptx::pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
   if (lane == 0) lse[(size_t)v * kH + h] = mx + logf(tot);
+}
+
+// The same for the sparse decode (one pair a part): one warp combines 128 of the 512 columns of row v and
+// head h, four columns a lane. The weights of up to 32 parts are found together, a part a lane, and the
+// parts' values are loaded eight at a time: with few rows cut over many pairs the merge is a chain of
+// loads, and this makes it a short one.
+__device__ __forceinline__ void merge_row_quarter(const int32_t* __restrict__ counts, int max_tiles, int G, long long T, int b0,
+                                                  int b1, int v, int h, int quarter, const float* __restrict__ part_o,
+                                                  const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ o_lat,
+                                                  float* __restrict__ lse) {
+  const int lane = threadIdx.x & 31;
+  long long off = 0;
+  for (int x = b0; x < min(b1, v); ++x) off += item_tiles<true>(counts, x, max_tiles);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) off += __shfl_xor_sync(0xffffffffu, off, o);
+  const long long tb = item_tiles<true>(counts, v, max_tiles);
+  if (tb == 0) return;
+  const int p0 = pair_of(off, T, G), p1 = pair_of(off + tb - 1, T, G);
+  if (p0 == p1) return;                       // written whole by one pair
+  auto slot = [&](int q) -> int {
+    const long long start_q = (long long)q * T / G;
+    if (q > p1 || (long long)(q + 1) * T / G <= start_q) return -1;
+    return q * 2 + (start_q < off ? 1 : 0);
+  };
+  float mx = -INFINITY;
+  for (int q0 = p0; q0 <= p1; q0 += 32) {
+    const int idx = slot(q0 + lane);
+    mx = fmaxf(mx, warp_max(idx >= 0 ? part_lse[(size_t)idx * kH + h] : -INFINITY));
+  }
+  const float mref = mx == -INFINITY ? 0.f : mx;
+  float tot = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q0 = p0; q0 <= p1; q0 += 32) {
+    const int idx = slot(q0 + lane);
+    const float w = idx >= 0 ? exp2f((part_lse[(size_t)idx * kH + h] - mref) * 1.4426950408889634f) : 0.f;
+    tot += warp_sum(w);
+    const int n = min(32, p1 - q0 + 1);
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = __shfl_sync(0xffffffffu, idx, (j0 + j) & 31);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + j < n && i >= 0)
+          x[j] = *(reinterpret_cast<const float4*>(part_o + ((size_t)i * kH + h) * kDC + 128 * quarter) + lane);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+        if (j0 + j < n && wj != 0.f) {
+          acc.x = fmaf(wj, x[j].x, acc.x);
+          acc.y = fmaf(wj, x[j].y, acc.y);
+          acc.z = fmaf(wj, x[j].z, acc.z);
+          acc.w = fmaf(wj, x[j].w, acc.w);
+        }
+      }
+    }
+  }
+  const float inv = tot != 0.f ? 1.f / tot : 0.f;
+  uint2* dst = reinterpret_cast<uint2*>(o_lat + ((size_t)v * kH + h) * kDC + 128 * quarter) + lane;
+  *dst = make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (quarter == 0 && lane == 0) lse[(size_t)v * kH + h] = tot != 0.f ? mref + logf(tot) : -INFINITY;
+}
+// All cut rows: (row, head, quarter) units dealt out over the grid's warps, neighbours to different SMs.
+__device__ __forceinline__ void merge_rows(const int32_t* __restrict__ counts, int rows, int max_tiles, int G, long long T,
+                                           int block, int blocks, int warps, const float* __restrict__ part_o,
+                                           const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ o_lat,
+                                           float* __restrict__ lse) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (rows + 31) / 32;
+  const int b0 = min(rows, lane * per), b1 = min(rows, b0 + per);
+  const long long units = (long long)rows * kH * 4;
+  for (long long u = (long long)warp * blocks + block; u < units; u += (long long)blocks * warps)
+    merge_row_quarter(counts, max_tiles, G, T, b0, b1, (int)(u / (kH * 4)), (int)(u % kH), (int)(u / kH % 4), part_o, part_lse,
+                      o_lat, lse);
 }
 
 // ---- bounded waits ---------------------------------------------------------------------------------
@@ -948,13 +1035,18 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
     // here (all waits above are bounded), so the barrier always completes.
     if (work[4] > 0 && work[5] == 0) {
       cooperative_groups::this_grid().sync();
-      const int per = (p.B + 31) / 32;
-      const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-      const int warps = kThreads / 32;
-      const long long units = (long long)p.B * p.s_q * kH;
-      for (long long u = (long long)blockIdx.x * warps + warp; u < units; u += (long long)gridDim.x * warps)
-        merge_token_head<kSparse>(lens, p.s_q, p.max_tiles, npairs / p.s_q, work[4], b0, b1, (int)(u / kH), (int)(u % kH),
-                         p.part_o, p.part_lse, p.o_lat, p.lse);
+      if constexpr (kSparse) {
+        merge_rows(lens, p.B, p.max_tiles, active_groups<true>(npairs, work[4]), work[4], (int)blockIdx.x, (int)gridDim.x,
+                   kThreads / 32, p.part_o, p.part_lse, p.o_lat, p.lse);
+      } else {
+        const int per = (p.B + 31) / 32;
+        const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+        const int warps = kThreads / 32;
+        const long long units = (long long)p.B * p.s_q * kH;
+        for (long long u = (long long)blockIdx.x * warps + warp; u < units; u += (long long)gridDim.x * warps)
+          merge_token_head(lens, p.s_q, p.max_tiles, npairs / p.s_q, work[4], b0, b1, (int)(u / kH), (int)(u % kH),
+                           p.part_o, p.part_lse, p.o_lat, p.lse);
+      }
     }
     allow_dependents();
   }
@@ -971,7 +1063,6 @@ merge_kernel(const int32_t* __restrict__ lens, int B, int s_q, int max_tiles, in
              const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ o_lat, float* __restrict__ lse) {
   // blocks stride over the new tokens v = b * s_q + tok; a token's parts come from pair (group, tok) of
   // the groups that covered its sequence's tiles
-  const int G = npairs / s_q;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_wait();
   allow_dependents();
@@ -992,9 +1083,15 @@ merge_kernel(const int32_t* __restrict__ lens, int B, int s_q, int max_tiles, in
     max_tb = max(max_tb, __shfl_xor_sync(0xffffffffu, max_tb, o));
   }
   const long long T = local;
+  const int G = active_groups<kSparse>(npairs / s_q, T);
   if (T == 0 || G == 0 || whole_sequences(B, G, T, max_tb)) return;   // nothing was cut
-  for (int v = blockIdx.x; v < B * s_q; v += gridDim.x)
-    merge_token_head<kSparse>(lens, s_q, max_tiles, G, T, b0, b1, v, blockIdx.y * kMergeHeads + warp, part_o, part_lse, o_lat, lse);
+  if constexpr (kSparse) {
+    merge_rows(lens, B, max_tiles, G, T, (int)(blockIdx.y * gridDim.x + blockIdx.x), (int)(gridDim.x * gridDim.y), kMergeHeads,
+               part_o, part_lse, o_lat, lse);
+  } else {
+    for (int v = blockIdx.x; v < B * s_q; v += gridDim.x)
+      merge_token_head(lens, s_q, max_tiles, G, T, b0, b1, v, blockIdx.y * kMergeHeads + warp, part_o, part_lse, o_lat, lse);
+  }
 }
 
 // ---- host side -----------------------------------------------------------------------------------------

@@ -16,7 +16,9 @@
 #include "gemm_sm100.cuh"
 #include "gqla_sm100.cuh"
 #include "cache8.cuh"
+#include "decode8_sm100.cuh"
 #include "pages.cuh"
+#include "score_sm100.cuh"
 
 namespace {
 
@@ -833,6 +835,7 @@ int mla_update_page_keys_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, i
 
 size_t mla_score_pages_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, int32_t max_pages) {
   if (check_dims(dims) || check_dtype(dtype) || !tokens_ok(B, s_q) || max_pages <= 0) return 0;
+  if (mla::score::supported(dims, dtype, (int64_t)B * s_q, max_pages)) return 0;
   return (size_t)B * s_q * dims->H * ((size_t)max_pages + 1) * sizeof(float);
 }
 
@@ -850,6 +853,9 @@ int mla_score_pages(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_
   const int W = dims->d_c + dims->d_r, H = dims->H, n_tok = B * s_q;
   if (!stride_ok(key_stride, dtype, W)) return MLA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (mla::score::supported(dims, dtype, n_tok, max_pages))
+    return mla::score::launch_score(dims, n_tok, s_q, q_abs, keys, key_stride, num_pages, block_table, max_pages, seqlens,
+                                    score_scale(dims), scores, num_sms(), st);
   using namespace mla::pages;
   if (!workspace || ws_bytes < mla_score_pages_workspace_size(dims, dtype, B, s_q, max_pages)) return MLA_ERR_WORKSPACE;
   const int64_t page_tiles = ((int64_t)max_pages + kScorePages - 1) / kScorePages;
@@ -963,6 +969,8 @@ int mla_decode_absorbed_sparse(const mla_dims_t* dims, int32_t dtype, int32_t B,
 
 size_t mla_decode_sparse_fp8_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, int32_t k) {
   if (check_dims(dims) || check_dtype(dtype) || !tokens_ok(B, s_q) || k <= 0) return 0;
+  if (mla::sm100::decode_supported(dims, dtype, B * s_q, 1))
+    return mla::sm100::decode_workspace_bytes(dims, dtype, B * s_q, 1, num_sms());
   return simt_decode_ws(B * s_q, dims->H, dims->d_c, k);
 }
 
@@ -973,6 +981,11 @@ int mla_decode_absorbed_sparse_fp8(const mla_dims_t* dims, int32_t dtype, int32_
   int rc = sparse_args(dims, dtype, B, s_q, q_abs, block_table, max_pages, seqlens, pages, counts, k, o_lat, lse,
                        workspace);
   if (rc || (rc = fp8_cache_args(dims, dtype, cache))) return rc;
+  if (mla::sm100::decode_supported(dims, dtype, B * s_q, 1)) {
+    const mla_dims_t dd = with_scale(dims);
+    return mla::sm100f8::launch_decode8(&dd, B * s_q, q_abs, cache, block_table, max_pages, seqlens, o_lat, lse, workspace,
+                                        ws_bytes, num_sms(), reinterpret_cast<cudaStream_t>(stream), {pages, counts, k, s_q});
+  }
   DecodeArgs A{};
   A.kpart = cache->codes; A.k_stride = cache->code_stride; A.kscale = cache->scales;
   A.vpart = cache->codes; A.v_stride = cache->code_stride;

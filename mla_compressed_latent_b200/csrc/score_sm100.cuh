@@ -1,0 +1,324 @@
+// Page scores on the sm_100a tensor cores.
+//
+//   u[h, p] = sm_scale q[h, :] · key_p          score[p] = sum_h exp(u[h, p] - logsumexp_p u[h, :])
+//
+// for every token v, over the pages p it sees. The softmax runs over the pages of one head and the sum over
+// the heads of one page, so a token needs all of u before it can write anything. u never leaves the
+// SM: the 128 heads are the M rows of the product and pages its N columns, and an accumulator of 128
+// lanes x 512 columns is exactly the tensor memory of one SM. A cluster of 1, 2, 4 or 8 CTAs takes one
+// token, up to 512 pages each; the CTAs swap each head's running maximum and sum through
+// distributed shared memory, and read their u a second time to sum the masses over the heads.
+// Bound: q (128 rows) and the keys, read once per token (keys of one sequence come from L2 after the first
+// token); 2 · 128 · (d_c + d_r) operations a page.
+//
+// Warps 0-7 gather the keys (a page's key lies wherever the block table says, so rows are fetched 16 bytes a
+// thread with asynchronous copies into 128-byte swizzled tiles of 64 pages x 64 columns, six stages
+// ahead), then turn the accumulator into masses; warp 8 loads q by TMA and issues the products.
+#pragma once
+
+#include "common.cuh"
+#include "gemm_sm100.cuh"
+#include "pages.cuh"
+#include "ptx_sm100.cuh"
+#include "tmap.cuh"
+
+namespace mla {
+namespace score {
+
+constexpr int kH = 128;               // accumulator rows: heads, padded
+constexpr int kTile = 64;             // pages per product
+constexpr int kMaxPages = 512;        // pages per CTA: the accumulator's columns
+constexpr int kMaxChunks = 9;         // 64-column chunks of a row of up to 576 values
+constexpr int kStages = 8;
+constexpr int kAhead = 6;             // stages a thread's copies run ahead of what it has handed over
+constexpr int kStageBytes = kTile * 128;
+constexpr int kQChunkBytes = kH * 128;
+constexpr int kWorkers = 256;         // threads of warps 0-7
+constexpr int kThreads = kWorkers + 32;
+constexpr int kMaxCluster = 8;
+constexpr int kOffRing = kMaxChunks * kQChunkBytes;
+constexpr int kOffStats = kOffRing + kStages * kStageBytes;            // float2 [cluster][2][kH]
+constexpr int kOffBar = kOffStats + kMaxCluster * 2 * kH * 8;
+enum Bar { FULL = 0, EMPTY = FULL + kStages, Q_FULL = EMPTY + kStages, DONE = Q_FULL + kMaxChunks, NUM_BARS };
+constexpr int kOffSlot = kOffBar + NUM_BARS * 8;
+constexpr int kSmemBytes = kOffSlot + 16 + 1024;   // + alignment slack of the dynamic base
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(4 * kMaxPages * 4 <= kOffRing, "the column sums fit the query's place");
+
+constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kH, kTile, false);
+
+struct Params {
+  const __nv_bfloat16* keys;
+  int64_t key_stride;
+  const int32_t* block_table;
+  int max_pages, num_pages;
+  const int32_t* seqlens;
+  int s_q, H, W;
+  float scale_log2;
+  float* scores;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  const uint32_t n = live ? 16u : 0u;   // 0: the 16 bytes are zeros and src is not read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory"); }
+
+__global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int v = (int)ptx::cluster_id_x();
+  const int csize = (int)(gridDim.x / ptx::num_clusters_x());
+  auto bar = [&](int i) -> uint32_t { return base + kOffBar + 8u * (uint32_t)i; };
+  volatile int* abort = reinterpret_cast<volatile int*>(gbase + kOffSlot + 8);
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) { ptx::mbar_init(bar(FULL + i), kWorkers); ptx::mbar_init(bar(EMPTY + i), 1); }
+    for (int i = 0; i < kMaxChunks; ++i) ptx::mbar_init(bar(Q_FULL + i), 1);
+    ptx::mbar_init(bar(DONE), 1);
+    *abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tm_q);
+  }
+  if (warp == 8) { ptx::tmem_alloc(base + kOffSlot, 512); ptx::tmem_relinquish(); }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + kOffSlot);
+  grid_dependency_wait();
+  allow_dependents();
+
+  // this CTA's pages: [p0, p0 + n) of the token's
+  const int seq = v / p.s_q;
+  int n_all = pages::visible_pages(p.seqlens[seq], p.s_q, v % p.s_q);
+  if (n_all > p.max_pages) {
+    if (tid == 0 && rank == 0) report(MLA_ERR_DEVICE_CHECK);
+    n_all = p.max_pages;
+  }
+  const int per = ((n_all + csize - 1) / csize + kTile - 1) / kTile * kTile;
+  const int p0 = min(n_all, (int)rank * per), n = min(n_all - p0, per);
+  const int tiles = (n + kTile - 1) / kTile, chunks = (p.W + 63) / 64, total = tiles * chunks;
+  float2* stats = reinterpret_cast<float2*>(gbase + kOffStats);
+
+  if (warp < 8) {
+    // ---- gather: rows r0 and r0 + 32 of each 64-page tile, one 16-byte piece of the chunk's 128 bytes
+    const int r0 = tid >> 3, piece = tid & 7;
+    const uint32_t dst0 = base + kOffRing + (uint32_t)r0 * 128u + (((uint32_t)piece ^ ((uint32_t)r0 & 7u)) << 4);
+    const int32_t* table = p.block_table + (int64_t)seq * p.max_pages + p0;
+    auto page_of = [&](int row) -> int { return row < n ? table[row] : -1; };
+    int next0 = page_of(r0), next1 = page_of(r0 + 32), pg0 = -1, pg1 = -1;
+    bool live = true;
+    for (int i = 0, kc = 0, tile = 0; i < total + kAhead; ++i) {
+      if (i < total && live) {
+        if (kc == 0) {   // a new tile: its page ids were read a tile ago
+          pg0 = next0;
+          pg1 = next1;
+          if (tile * kTile + r0 < n && (pg0 < 0 || pg0 >= p.num_pages)) { report(MLA_ERR_DEVICE_CHECK); pg0 = -1; }
+          if (tile * kTile + r0 + 32 < n && (pg1 < 0 || pg1 >= p.num_pages)) { report(MLA_ERR_DEVICE_CHECK); pg1 = -1; }
+          next0 = page_of((tile + 1) * kTile + r0);
+          next1 = page_of((tile + 1) * kTile + r0 + 32);
+        }
+        const int s = i % kStages;
+        if (i >= kStages) live = gemm::wait(bar(EMPTY + s), ((i / kStages) & 1u) ^ 1u, abort);
+        if (live) {
+          const int col = kc * 64 + piece * 8;
+          const bool in = col < p.W;
+          const uint32_t dst = dst0 + (uint32_t)s * kStageBytes;
+          const __nv_bfloat16* k0 = p.keys + (int64_t)max(pg0, 0) * p.key_stride + (in ? col : 0);
+          const __nv_bfloat16* k1 = p.keys + (int64_t)max(pg1, 0) * p.key_stride + (in ? col : 0);
+          cp_async16(dst, k0, in && pg0 >= 0);
+          cp_async16(dst + 32 * 128, k1, in && pg1 >= 0);
+        }
+        if (++kc == chunks) { kc = 0; ++tile; }
+      }
+      cp_async_commit();
+      if (i >= kAhead && live) {   // this thread's copies of stage i - kAhead have landed: hand it over
+        cp_async_wait<kAhead>();
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(bar(FULL + (i - kAhead) % kStages));
+      }
+    }
+    cp_async_wait<0>();
+    if (!live) *abort = 1;
+    // ---- per head (= lane of the accumulator): maximum and sum of exponentials over this CTA's pages; warps
+    // 0-3 take the even tiles, 4-7 the odd ones
+    __syncwarp();
+    const int q4 = warp & 3, half = warp >> 2, head = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const bool ok = __all_sync(0xffffffffu, gemm::wait(bar(DONE), 0, abort));
+    ptx::tc_fence_after();
+    const float s2 = p.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    for (int t = half; t < tiles && ok; t += 2) {
+      const int valid = n - t * kTile;
+#pragma unroll 1
+      for (int c = 0; c < kTile; c += 32) {
+        uint32_t r[32];
+        ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c), r);
+        ptx::tmem_wait_ld_regs(r);
+        float mt = m;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c + j < valid) mt = fmaxf(mt, __uint_as_float(r[j]));
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c + j < valid) sum += ptx::ex2_approx((__uint_as_float(r[j]) - mt) * s2);
+        if (c < valid) {
+          l = l * ptx::ex2_approx((m - mt) * s2) + sum;
+          m = mt;
+        }
+      }
+    }
+    for (int r = 0; r < csize; ++r) {
+      const uint32_t at = ptx::map_to_cta(base + kOffStats + (uint32_t)(((int)rank * 2 + half) * kH + head) * 8u, (uint32_t)r);
+      ptx::st_cluster_f32(at, m);
+      ptx::st_cluster_f32(at + 4u, l);
+    }
+  } else {
+    // ---- q by TMA, one barrier per 64-column chunk, then the products
+    if (lane == 0 && tiles > 0) {
+      for (int kc = 0; kc < chunks; ++kc) {
+        ptx::mbar_arrive_expect_tx(bar(Q_FULL + kc), kQChunkBytes);
+        ptx::tma_load_2d(base + kc * kQChunkBytes, &tm_q, kc * 64, v * p.H, bar(Q_FULL + kc));
+        ptx::tma_load_2d(base + kc * kQChunkBytes + kQChunkBytes / 2, &tm_q, kc * 64, v * p.H + 64, bar(Q_FULL + kc));
+      }
+    }
+    __syncwarp();
+    const uint64_t qd = ptx::smem_desc_sw128(base, 16, 1024), kd = ptx::smem_desc_sw128(base + kOffRing, 16, 1024);
+    bool live = true;
+    for (int i = 0, kc = 0, tile = 0; i < total && live; ++i) {
+      const int s = i % kStages;
+      if (tile == 0) live = __all_sync(0xffffffffu, gemm::wait(bar(Q_FULL + kc), 0, abort));
+      live = live && __all_sync(0xffffffffu, gemm::wait(bar(FULL + s), (i / kStages) & 1u, abort));
+      if (live && ptx::elect_one()) {
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ptx::mma_ss(tmem + (uint32_t)(tile * kTile), qd + (uint64_t)(kc * (kQChunkBytes >> 4) + 2 * k),
+                      kd + (uint64_t)(s * (kStageBytes >> 4) + 2 * k), kIdesc, (kc | k) ? 1u : 0u);
+        ptx::mma_commit(bar(EMPTY + s));
+        if (i == total - 1) ptx::mma_commit(bar(DONE));
+      }
+      __syncwarp();
+      if (++kc == chunks) { kc = 0; ++tile; }
+    }
+    if (total == 0 && lane == 0) ptx::mbar_arrive(bar(DONE));
+    if (!live) {
+      *abort = 1;
+      if (ptx::elect_one()) ptx::mma_commit(bar(DONE));   // what was issued completes before the exit
+      for (int kc = 0; kc < chunks; ++kc) gemm::wait(bar(Q_FULL + kc), 0);   // and so do the loads
+      gemm::wait(bar(DONE), 0);
+    }
+    __syncwarp();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();   // every CTA's statistics are in place
+  ptx::tc_fence_after();
+  if (warp < 8 && !*abort) {
+    const int q4 = warp & 3, half = warp >> 2, head = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const float s2 = p.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    for (int r = 0; r < 2 * csize; ++r) m = fmaxf(m, stats[r * kH + head].x);
+    for (int r = 0; r < 2 * csize; ++r) {
+      const float2 st = stats[r * kH + head];
+      if (st.y != 0.f) l += st.y * ptx::ex2_approx((st.x - m) * s2);
+    }
+    const float inv = head < p.H ? 1.f / l : 0.f;
+    // masses e^(u - m) / l, summed over the warp's 32 heads: at each step a lane keeps half of its columns and
+    // adds the other lane's values of them, so that lane j ends with column j
+    float* colsum = reinterpret_cast<float*>(gbase);   // [4][kMaxPages], over the query (its products are done)
+    for (int t = half; t < tiles; t += 2) {
+#pragma unroll 1
+      for (int c = 0; c < kTile; c += 32) {
+        if (t * kTile + c >= n) break;
+        uint32_t r[32];
+        ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c), r);
+        ptx::tmem_wait_ld_regs(r);
+        float a[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float e = ptx::ex2_approx((__uint_as_float(r[j]) - m) * s2) * inv;
+          a[j] = head < p.H ? e : 0.f;   // (rows past the last head may hold anything)
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const bool up = (lane & o) != 0;
+#pragma unroll
+          for (int j = 0; j < o; ++j) {
+            const float send = up ? a[j] : a[j + o], keep = up ? a[j + o] : a[j];
+            a[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+        colsum[q4 * kMaxPages + t * kTile + c + lane] = a[0];
+      }
+    }
+    ptx::tc_fence_before();
+    ptx::named_bar_sync(1, kWorkers);
+    float* out = p.scores + (int64_t)v * p.max_pages + p0;
+    for (int i = tid; i < n; i += kWorkers)
+      out[i] = (colsum[i] + colsum[kMaxPages + i]) + (colsum[2 * kMaxPages + i] + colsum[3 * kMaxPages + i]);
+  }
+  __syncthreads();
+  if (warp == 8) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+inline bool supported(const mla_dims_t* d, int32_t dtype, int64_t rows, int32_t max_pages) {
+  const int W = d->d_c + d->d_r;
+  return dtype == MLA_BF16 && d->H <= kH && W >= 64 && W <= 64 * kMaxChunks && W % 8 == 0 && max_pages <= kMaxCluster * kMaxPages &&
+         rows * d->H <= INT32_MAX && rows * kMaxCluster <= INT32_MAX;
+}
+
+inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const void* q_abs, const void* keys, int64_t key_stride,
+                        int32_t num_pages, const int32_t* block_table, int32_t max_pages, const int32_t* seqlens,
+                        float scale, float* scores, int num_sms, cudaStream_t st) {
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    if (cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  const int W = d->d_c + d->d_r;
+  CUtensorMap tm_q;   // q_abs as [rows * H, W]: boxes of 64 heads x 64 columns
+  if (!tmap::make_bf16_sw128(&tm_q, q_abs, W, (int64_t)rows * d->H, W, 64)) return MLA_ERR_INVALID_ARG;
+  // as few CTAs a token as hold its pages, doubled while the tokens leave SMs idle and a CTA would still
+  // have a whole tile
+  int c = 1;
+  while (c < kMaxCluster && c * kMaxPages < max_pages) c *= 2;
+  while (c < kMaxCluster && (int64_t)rows * 2 * c <= num_sms && max_pages > c * kTile) c *= 2;
+  Params prm{reinterpret_cast<const __nv_bfloat16*>(keys), key_stride, block_table, max_pages, num_pages, seqlens, s_q,
+             d->H, W, scale * 1.4426950408889634f, scores};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * c));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, score_kernel, tm_q, prm);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace score
+}  // namespace mla

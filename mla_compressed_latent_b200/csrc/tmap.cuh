@@ -41,5 +41,19 @@ inline bool make_bf16_sw128(CUtensorMap* m, const void* base, int64_t cols, int6
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A row-major matrix of bytes [rows, cols] with a row stride of `stride` bytes, read in boxes of 128 columns
+// (one 128-byte swizzle row) x box_rows rows.
+inline bool make_u8_sw128(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t stride, int box_rows) {
+  const EncodeTiledFn encode = encode_tiled_fn();
+  if (!encode || rows <= 0 || cols <= 0) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace tmap
 }  // namespace mla

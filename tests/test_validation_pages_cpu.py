@@ -13,7 +13,7 @@ from mla_compressed_latent_b200 import ops
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(),
                                 reason="fake device pointers: host-side checks run where no GPU is visible")
 
-GOOD, ODD, BIG_WS = 4096, 4100, 1 << 40
+GOOD, ODD, BIG_WS = 4096, 4100, 1 << 50
 
 
 @pytest.fixture(scope="module")
@@ -54,7 +54,7 @@ CALLS = {
     "mla_decode_absorbed_sparse": ([1, 64, 1, "P", "LC", "P", 64, "P", "P", "P", 16, "P", "P", "P", BIG_WS, None],
                                    [3, 5, 7, 8, 9, 11, 12], [1, 2, 6, 10], 13, []),
     "mla_decode_absorbed_sparse_fp8": ([1, 64, 1, "P", "FC", "P", 64, "P", "P", "P", 16, "P", "P", "P", BIG_WS, None],
-                                       [3, 5, 7, 8, 9, 11, 12], [1, 2, 6, 10], None, [13]),
+                                       [3, 5, 7, 8, 9, 11, 12], [1, 2, 6, 10], 13, []),
 }
 
 
