@@ -375,35 +375,59 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           // (the tile's scales landed with its rows, before its products)
           if (!wait_bar_warp(bar(S_FULL + sb), (it / kSBufs) & 1u, abort_addr, false)) { ok = false; continue; }
           const int valid = L - t * kTile;
-          float x[64];
+          if (valid < kTile) {   // slots past the end weigh nothing, whatever the cache holds there
+            for (int j = max(valid, 0) + lane; j < kTile; j += 32) ptx::st_shared_u32(sc_addr + 4u * j, 0u);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+          }
+          float smax = 0.f;
+          uint64_t x2[32];   // x of positions 2 i, 2 i + 1
+          const uint64_t unit2 = ptx::pack_f32x2(q_unit, q_unit);
           ptx::tc_fence_after();
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t vc[32], vr[32];
             ptx::tmem_ld32(tmem + lane_off + kSCol0 + 128u * sb + 32u * half, vc);
             ptx::tmem_ld32(tmem + lane_off + kSCol0 + 128u * sb + 64u + 32u * half, vr);
+            if (half == 0) {
+              const float s0 = __uint_as_float(ptx::ld_shared_u32(sc_addr + 4u * lane));
+              const float s1 = __uint_as_float(ptx::ld_shared_u32(sc_addr + 4u * (lane + 32)));
+              smax = warp_max(fmaxf(fabsf(s0), fabsf(s1)));
+            }
             ptx::tmem_wait_ld_regs(vc);
             ptx::tmem_wait_ld_regs(vr);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const uint4 s4 = ptx::ld_shared_v4(sc_addr + 4u * (32 * half + j));
-              x[32 * half + j] = fmaf(__uint_as_float(vc[j]), __uint_as_float(s4.x) * q_unit, __uint_as_float(vr[j]));
-              x[32 * half + j + 1] = fmaf(__uint_as_float(vc[j + 1]), __uint_as_float(s4.y) * q_unit, __uint_as_float(vr[j + 1]));
-              x[32 * half + j + 2] = fmaf(__uint_as_float(vc[j + 2]), __uint_as_float(s4.z) * q_unit, __uint_as_float(vr[j + 2]));
-              x[32 * half + j + 3] = fmaf(__uint_as_float(vc[j + 3]), __uint_as_float(s4.w) * q_unit, __uint_as_float(vr[j + 3]));
+              uint64_t sa, sb2;
+              ptx::ld_shared_v2u64(sc_addr + 4u * (32 * half + j), &sa, &sb2);
+              x2[(32 * half + j) / 2] = ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(vc[j]), __uint_as_float(vc[j + 1])),
+                                                       ptx::mul_f32x2(sa, unit2),
+                                                       ptx::pack_f32x2(__uint_as_float(vr[j]), __uint_as_float(vr[j + 1])));
+              x2[(32 * half + j) / 2 + 1] =
+                  ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(vc[j + 2]), __uint_as_float(vc[j + 3])),
+                                 ptx::mul_f32x2(sb2, unit2),
+                                 ptx::pack_f32x2(__uint_as_float(vr[j + 2]), __uint_as_float(vr[j + 3])));
             }
           }
           ptx::tc_fence_before();
           ptx::mbar_arrive(bar(S_EMPTY + sb));
-          const float s_lo = lane < valid ? __uint_as_float(ptx::ld_shared_u32(sc_addr + 4u * lane)) : 0.f;
-          const float s_hi = lane + 32 < valid ? __uint_as_float(ptx::ld_shared_u32(sc_addr + 4u * (lane + 32))) : 0.f;
-          const float smax = warp_max(fmaxf(fabsf(s_lo), fabsf(s_hi)));
+          if (valid < kTile) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float x0, x1;
+              ptx::unpack_f32x2(x2[i], &x0, &x1);
+              x2[i] = ptx::pack_f32x2(2 * i < valid ? x0 : -INFINITY, 2 * i + 1 < valid ? x1 : -INFINITY);
+            }
+          }
           // 2^E above every scale (E at least -100: smaller scales weigh nothing, and e stays finite)
           const float e_tile = (float)max((int)(__float_as_uint(smax) >> 23) - 126, -100);
           float a4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (valid >= kTile || j < valid) a4[j & 3] = fmaxf(a4[j & 3], x[j]);
+          for (int i = 0; i < 32; ++i) {
+            float x0, x1;
+            ptx::unpack_f32x2(x2[i], &x0, &x1);
+            a4[i & 3] = fmaxf(a4[i & 3], fmaxf(x0, x1));
+          }
           // the reference this tile needs: its weights below 2^kTopLog2
           const float need = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3])) * scale2 + e_tile - kTopLog2;
           float m_prev = -INFINITY;
@@ -422,27 +446,38 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
             l_own = (m_own == -INFINITY) ? 0.f : l_own * ptx::ex2_approx(m_own - m_new);
             m_own = m_new;
           }
-          // e, its sum, and w = e s in two E4M3 terms
+          // e, its sum, and w = e s in two E4M3 terms, sixteen positions at a time
           uint32_t hi[16], lo[16];
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t l2[2] = {0ull, 0ull};
+          const uint64_t scale22 = ptx::pack_f32x2(scale2, scale2), neg_m2 = ptx::pack_f32x2(-m_new, -m_new);
 #pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const uint4 s4 = ptx::ld_shared_v4(sc_addr + 4u * j);
-            const uint32_t sj[4] = {s4.x, s4.y, s4.z, s4.w};
-            float w[4];
+          for (int c = 0; c < 4; ++c) {
+            uint64_t e2[8], s2[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const bool in = valid >= kTile || j + u < valid;
-              const float e = in ? ptx::ex2_approx(fmaf(x[j + u], scale2, -m_new)) : 0.f;
-              ls[u] += e;
-              w[u] = in ? e * __uint_as_float(sj[u]) : 0.f;
+            for (int i = 0; i < 8; i += 2) ptx::ld_shared_v2u64(sc_addr + 4u * (16 * c + 2 * i), &s2[i], &s2[i + 1]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x0, x1;
+              ptx::unpack_f32x2(ptx::fma_f32x2(x2[8 * c + i], scale22, neg_m2), &x0, &x1);
+              e2[i] = ptx::pack_f32x2(ptx::ex2_approx(x0), ptx::ex2_approx(x1));
             }
-            uint32_t h0, l0, h1, l1;
-            split_e4m3x2(w[0], w[1], &h0, &l0);
-            split_e4m3x2(w[2], w[3], &h1, &l1);
-            hi[j >> 2] = h0 | (h1 << 16);
-            lo[j >> 2] = l0 | (l1 << 16);
+            uint32_t h8[8], l8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              l2[i & 1] = ptx::add_f32x2(l2[i & 1], e2[i]);
+              float w0, w1;
+              ptx::unpack_f32x2(ptx::mul_f32x2(e2[i], s2[i]), &w0, &w1);
+              split_e4m3x2(w0, w1, &h8[i], &l8[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              hi[4 * c + i / 2] = __byte_perm(h8[i], h8[i + 1], 0x5410);
+              lo[4 * c + i / 2] = __byte_perm(l8[i], l8[i + 1], 0x5410);
+            }
           }
+          float ls[4];
+          ptx::unpack_f32x2(l2[0], &ls[0], &ls[1]);
+          ptx::unpack_f32x2(l2[1], &ls[2], &ls[3]);
           l_own += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           if (!__all_sync(0xffffffffu, stg_free) &&
               !wait_bar_warp(bar(STG_FREE + stg), ((it / kStaging) & 1u) ^ 1u, abort_addr, true)) {
