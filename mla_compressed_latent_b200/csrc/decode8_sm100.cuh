@@ -3,25 +3,26 @@
 //
 //   S[h, j] = s_j (q_h · code_j) + q_r,h · k_r,j        O[h, :] = sum_j (P[h, j] s_j) code_j
 //
-// The codes are the B operand of both products as they lie in the cache: E4M3 rows of 512 bytes, read
-// K-major for S and MN-major for O. A row's scale s_j multiplies a column of S and a column of P, so no
-// dequantised row is ever made and the cache's bytes cross the memory system once, at 644 a
-// position where 16-bit rows take 1152. An E4M3 product wants E4M3 on the other side too. Four
-// significant bits are too few for a query or a weight, but two terms hold eight:
-//   q 2^t = q_hi + q_lo, the nearest E4M3 value and the nearest to what is left. t brings the head's
-//     largest value to 128..256; the sum is the bf16 value itself down to a thousandth of that, and off
-//     by at most 2^-10 (2^-18 of the largest) below;
-//   w = P s 2^g = w_hi + w_lo likewise, w <= 256: within 2^-8 of each weight and 2^-10 of the 256.
-// An 8-bit product of K = 32 takes the time of a 16-bit one of K = 16, so two of them cost what the
-// 16-bit decode pays for the same rows, with half the bytes to load and to keep in shared memory.
+// A row's scale s_j multiplies a column of S and a column of P, so no dequantised row is ever made
+// and the cache's bytes cross the memory system once, at 644 a position where 16-bit rows take 1152.
+// S is an E4M3 product of the codes as they lie in the cache (K-major). It wants E4M3 queries too, and
+// four significant bits are too few, but two terms hold eight: q 2^t = q_hi + q_lo, the nearest E4M3
+// value and the nearest to what is left. t brings the head's largest value to 128..256; the sum is
+// the bf16 value itself down to a thousandth of that, and off by at most 2^-10 (2^-18 of the
+// largest) below. An 8-bit product of K = 32 takes the time of a 16-bit one of K = 16, so the two terms cost
+// what the 16-bit decode pays, with half the bytes to load and to keep in shared memory.
+// O is an fp16 product: the output CTA's row warps widen the codes (every E4M3 value is an fp16 value)
+// on their way into shared memory, and the weights w = P s are rounded to fp16's 11 bits. (An E4M3
+// product there, with the weights in two terms, would read the codes MN-major; 8-bit MN-major operands
+// ran at a third of the rate: 380 cycles for M = 128, N = 256, K = 32, against 128.)
 //
 // The frame is that of decode_sm100.cuh: a pair of CTAs per worker (the score CTA holds q_hi and q_lo in
 // 256 TMEM columns and two score buffers of 64 + 64, the latents' products and the RoPE keys' apart
 // because only the former are scaled; the output CTA holds O in 512), eight row warps in two sets on
-// alternate tiles, P tiles handed over by bulk copies (hi and lo halves of a 128-byte row), lazy running
-// maxima, ranges of tiles per pair and one merge of cut rows. The reference M of a row's exponentials
-// includes the scales: e = 2^(x - M) with M >= max_j x_j + E - 8 and 2^E above the tile's scales, so that
-// w = e s stays below 2^8; l sums the same e, and O / l and M + log2 l need no correction.
+// alternate tiles, P tiles handed over by bulk copies, lazy running maxima, ranges of tiles per pair and one
+// merge of cut rows. The reference M of a row's exponentials includes the scales: e = 2^(x - M) with
+// M >= max_j x_j + E - 14 and 2^E above the tile's scales, so that w = e s stays below 2^14; l sums the
+// same e, and O / l and M + log2 l need no correction.
 #pragma once
 
 #include "cache8.cuh"
@@ -49,20 +50,21 @@ constexpr int kScaleBytes = kTile * 4;                 // the tile's 64 scales
 // tile i are done. Tile i + 8 is loaded once the products of tile i + 4 are, which waited for the
 // scores of tile i + 2 to be read, and a set reads those after it has finished tile i.
 constexpr int kScaleSlots = 2 * kKStages;
-constexpr int kVStages = 4;                            // output CTA: code boxes only
-constexpr int kVStageBytes = kCodeBoxes * kBoxBytes;   // 32768
+constexpr int kVStages = 2;                            // output CTA: tiles of fp16 values
+constexpr int kVChunks = kDC / 64;                     // 8 chunks of 64 rows x 64 values
+constexpr int kVStageBytes = kVChunks * kBoxBytes;     // 65536
 constexpr int kQBoxes = 2 * (kDC / 64);                // the query's latent part: 16 boxes of 64 heads x 64 columns
 constexpr int kSBufs = 2;
 constexpr int kSCol0 = 256;                            // buffer b: latent products at 256 + 128 b, RoPE products 64 on
 constexpr int kTmemCols = 512;
 constexpr int kPSlots = 4, kStaging = 2;
-constexpr int kPBytes = kH * 128;                      // a P tile: per row 64 hi codes, then 64 lo codes
+constexpr int kPBytes = kH * kTile * 2;                // a P tile: fp16 weights
 constexpr int kAlphaOff = kPBytes;
 constexpr int kCopyBytes = kPBytes + kH * 4;
 constexpr int kStgStride = kCopyBytes;
 constexpr int kSlotStride = 17408;                     // a multiple of 1024 (the swizzle repeat)
-// M moves when a tile would take a weight past 2^8; it then leaves room for 2^2 more
-constexpr float kTopLog2 = 8.0f, kRoomLog2 = 2.0f;
+// M moves when a tile would take a weight past 2^14; it then leaves room for 2^8 more
+constexpr float kTopLog2 = 14.0f, kRoomLog2 = 8.0f;
 
 constexpr int kOffK = 0;
 constexpr int kOffQR = kKStages * kKStageBytes;                       // the query's RoPE part, two boxes
@@ -95,7 +97,7 @@ static_assert(kOffQR % 1024 == 0 && kOffPSlots % 1024 == 0 && kKStageBytes % 102
 
 constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(kH, kTile, false);   // q · codeᵀ (K-major B)
 constexpr uint32_t kIdescR = ptx::idesc_bf16_f32(kH, kTile, false);   // q_r · k_rᵀ
-constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(kH, 256, true);      // w · code (MN-major B)
+constexpr uint32_t kIdescO = ptx::idesc_f16_f32(kH, 256, true);       // w · value (MN-major B)
 
 struct Params {
   const int32_t* block_table;
@@ -105,6 +107,8 @@ struct Params {
   const int32_t* page_list;
   const int32_t* counts;
   int k, s_q;                  // rows per sequence
+  const uint8_t* codes;
+  int64_t code_stride;
   const float* scales;
   __nv_bfloat16* o_lat;        // [rows, 128, 512]
   float* lse;                  // [rows, 128]
@@ -114,8 +118,8 @@ struct Params {
   int merge_in_kernel;
 };
 
-// w of two neighbouring positions as E4M3 pairs: hi = the nearest values, lo = the nearest to what is
-// left of the fp16 values (w <= 256 has 11 bits there; the difference is exact in fp16).
+// Two values as E4M3 pairs: hi = the nearest values, lo = the nearest to what is left of the fp16 values
+// (of bf16 values below 2^8, fp16 keeps everything but what is under 2^-24; the difference is exact).
 __device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t* hi, uint32_t* lo) {
   uint32_t h16, b16, d16;
   uint16_t h8, l8;
@@ -129,8 +133,8 @@ __device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t* hi, u
 }
 
 // Warp roles.  Score CTA: 0 TMA producer | 1, 2 S-MMA issuers of even and odd tiles (2 owns TMEM) | 3
-// copier | 4-11 row warps. Output CTA: 0 TMA producer | 1 O-MMA issuer | 2 receiver | 3 rows without pages
-// | 4-11 rescale and epilogue.
+// copier | 4-11 row warps. Output CTA: 1 O-MMA issuer | 2 receiver (and TMEM) | 3 rows without pages | 4-11 widening,
+// rescale and epilogue.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_rope,
                const __grid_constant__ CUtensorMap tm_q, const Params p) {
@@ -159,7 +163,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
     for (int i = 0; i < kStaging; ++i) { ptx::mbar_init(bar(P_WRITTEN + i), kH); ptx::mbar_init(bar(STG_FREE + i), 1); }
     ptx::mbar_init(bar(DEC_FULL), kH);
     ptx::mbar_init(bar(STATS_EMPTY), kGroup);
-    for (int i = 0; i < kVStages; ++i) { ptx::mbar_init(bar(V_FULL + i), 1); ptx::mbar_init(bar(V_EMPTY + i), 1); }
+    for (int i = 0; i < kVStages; ++i) { ptx::mbar_init(bar(V_FULL + i), kGroup); ptx::mbar_init(bar(V_EMPTY + i), 1); }
     ptx::mbar_init(bar(STATS_FULL), kH);
     *reinterpret_cast<volatile int*>(gbase + kOffAbort) = 0;
     ptx::fence_mbar_init();
@@ -446,8 +450,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
             l_own = (m_own == -INFINITY) ? 0.f : l_own * ptx::ex2_approx(m_own - m_new);
             m_own = m_new;
           }
-          // e, its sum, and w = e s in two E4M3 terms, sixteen positions at a time
-          uint32_t hi[16], lo[16];
+          // e, its sum, and w = e s, sixteen positions at a time
+          uint32_t pk[32];
           uint64_t l2[2] = {0ull, 0ull};
           const uint64_t scale22 = ptx::pack_f32x2(scale2, scale2), neg_m2 = ptx::pack_f32x2(-m_new, -m_new);
 #pragma unroll
@@ -461,18 +465,12 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
               ptx::unpack_f32x2(ptx::fma_f32x2(x2[8 * c + i], scale22, neg_m2), &x0, &x1);
               e2[i] = ptx::pack_f32x2(ptx::ex2_approx(x0), ptx::ex2_approx(x1));
             }
-            uint32_t h8[8], l8[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               l2[i & 1] = ptx::add_f32x2(l2[i & 1], e2[i]);
               float w0, w1;
               ptx::unpack_f32x2(ptx::mul_f32x2(e2[i], s2[i]), &w0, &w1);
-              split_e4m3x2(w0, w1, &h8[i], &l8[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              hi[4 * c + i / 2] = __byte_perm(h8[i], h8[i + 1], 0x5410);
-              lo[4 * c + i / 2] = __byte_perm(l8[i], l8[i + 1], 0x5410);
+              pk[8 * c + i] = ptx::pack_f16x2(w0, w1);
             }
           }
           float ls[4];
@@ -484,14 +482,12 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
             ok = false;
             continue;
           }
-          // the row [64 hi | 64 lo] into the K-major, 128-byte swizzled tile, and its rescale factor
+          // the row into the K-major, 128-byte swizzled tile, and its rescale factor
           const uint32_t st0 = base + kOffStaging + stg * kStgStride;
           const uint32_t prow = st0 + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            ptx::st_shared_v4(prow + (((uint32_t)c ^ (uint32_t)(row & 7)) << 4), hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-            ptx::st_shared_v4(prow + (((uint32_t)(c + 4) ^ (uint32_t)(row & 7)) << 4), lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-          }
+          for (int c = 0; c < 8; ++c)
+            ptx::st_shared_v4(prow + (((uint32_t)c ^ (uint32_t)(row & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
           reinterpret_cast<float*>(gbase + kOffStaging + stg * kStgStride + kAlphaOff)[row] = al;
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(bar(P_WRITTEN + stg));
@@ -536,24 +532,6 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           }
         }
       }
-    } else if (warp == 0) {
-      if (lane == 0) {   // ---- TMA producer: the codes of each tile
-        uint32_t it = 0;
-        bool ok = true;
-        while (ok && next()) {
-          for (int t = t_lo; t < t_hi; ++t, ++it) {
-            const uint32_t s = it % kVStages;
-            const int page = page_at(b, t, false);   // reported by the score CTA
-            if (!(ok = wait_bar(bar(V_EMPTY + s), ((it / kVStages) & 1u) ^ 1u, abort_addr, false))) break;
-            const uint32_t dst = base + kOffV + s * kVStageBytes;
-            ptx::mbar_arrive_expect_tx(bar(V_FULL + s), kVStageBytes);
-            for (int j = 0; j < kCodeBoxes; ++j)
-              ptx::tma_load_2d(dst + j * kBoxBytes, &tm_codes, 128 * j, page * kTile, bar(V_FULL + s));
-          }
-        }
-        for (uint32_t i = (it > (uint32_t)kVStages ? it - kVStages : 0); i < it; ++i)
-          wait_bar(bar(V_FULL + i % kVStages), (i / kVStages) & 1u, abort_addr, false, false);
-      }
     } else if (warp == 3) {
       // ---- rows that list no page attend nothing: zeros and lse = -inf
       for (int v = pair; v < p.rows; v += npairs) {
@@ -563,51 +541,27 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
         for (int i = lane; i < kH; i += 32) p.lse[(size_t)v * kH + i] = -INFINITY;
       }
     } else if (warp == 1) {
-      // ---- MMA issuer: O += w · code for the hi half, then the lo half of the weights; K = 64 positions in
-      // steps of 32 per half, N = 512 in 2 halves
+      // ---- MMA issuer: O += w · value, K = 64 positions in steps of 16, N = 512 in 2 halves
       const uint64_t v_desc0 = ptx::smem_desc_sw128(base + kOffV, kBoxBytes, 1024);
       const uint64_t p_desc0 = ptx::smem_desc_sw128(base + kOffPSlots, 16, 1024);
       uint32_t it = 0;
       bool ok = true;
       while (ok && next()) {
-        const int L = vlen(b);
         for (int t = t_lo; t < t_hi; ++t, ++it) {
           const uint32_t slot = it % kPSlots, s = it % kVStages;
-          if (!(ok = wait_bar_warp(bar(P_LOCAL + slot), (it / kPSlots) & 1u, abort_addr, false))) break;
           if (!(ok = wait_bar_warp(bar(V_FULL + s), (it / kVStages) & 1u, abort_addr, false))) break;
-          // a tile that ends inside its page: whole 32-row steps past the end are skipped, and the rows of the
-          // last step past it are zeroed (a code there may be NaN, and 0 * NaN = NaN)
-          int nk = kTile / 32;
-          if (L - t * kTile < kTile) {
-            const int valid = max(0, L - t * kTile);
-            nk = max(1, (valid + 31) / 32);
-            const int zr = nk * 32 - valid;
-            if (zr > 0) {
-              uint8_t* vst = gbase + kOffV + s * kVStageBytes;
-              for (int i = lane; i < zr * kCodeBoxes * 8; i += 32) {
-                const int r = valid + i / (kCodeBoxes * 8), rest = i % (kCodeBoxes * 8);
-                reinterpret_cast<uint4*>(vst + (rest / 8) * kBoxBytes + r * 128)[rest % 8] = make_uint4(0, 0, 0, 0);
-              }
-              ptx::fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
+          if (!(ok = wait_bar_warp(bar(P_LOCAL + slot), (it / kPSlots) & 1u, abort_addr, false))) break;
           if (ptx::elect_one()) {
             ptx::fence_proxy_async_smem();
             ptx::tc_fence_after();
             const uint64_t pd = p_desc0 + (uint64_t)(slot * (kSlotStride >> 4));
             const uint64_t vd = v_desc0 + (uint64_t)(s * (kVStageBytes >> 4));
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int kk = 0; kk < kTile / 32; ++kk) {
-                if (kk < nk) {
-                  const uint32_t acc = (t > t_lo || part > 0 || kk > 0) ? 1u : 0u;
-                  const uint64_t a = pd + (uint64_t)(4 * part + 2 * kk);
-                  ptx::mma_ss_f8(tmem, a, vd + (uint64_t)(kk * (32 * 128 >> 4)), kIdescO, acc);
-                  ptx::mma_ss_f8(tmem + 256, a, vd + (uint64_t)((2 * kBoxBytes >> 4) + kk * (32 * 128 >> 4)), kIdescO, acc);
-                }
-              }
+            for (int kk = 0; kk < kTile / 16; ++kk) {
+              const uint32_t acc = (t > t_lo || kk > 0) ? 1u : 0u;
+              ptx::mma_ss(tmem, pd + 2 * kk, vd + 128 * kk, kIdescO, acc);
+              ptx::mma_ss(tmem + 256, pd + 2 * kk, vd + 2048 + 128 * kk, kIdescO, acc);
+            }
             ptx::mma_commit(bar(V_EMPTY + s));
             ptx::mma_commit_mc(bar(P_EMPTY + slot), (uint16_t)0x3);
           }
@@ -615,8 +569,12 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
         }
       }
     } else if (warp >= 4) {
-      // ---- row warps: rescale of the warp's 16 rows of O before a tile whose weights have a newer
-      // reference, and the segment epilogue
+      // ---- row warps: each tile's codes widened to fp16 on their way into shared memory, rescale of the
+      // warp's 16 rows of O before a tile whose weights have a newer reference, and the segment epilogue.
+      // Warp w takes latents [64 w', + 64) (w' = w - 4), eight rows at a time, 16 codes a thread: the loads
+      // read whole 32-byte sectors and the stores of a warp spread over all banks. A tile's codes are
+      // loaded into registers while the tile before it is widened, its page is looked up one tile
+      // earlier still; the loads mostly hit L2, where the score CTA's reads have brought the rows.
       const int sub = (warp - 4) >> 2, qd = warp & 3;
       const int r0 = 32 * qd + 16 * sub + (lane >> 2);                       // and r0 + 8
       const uint32_t s_lane = (uint32_t)(32 * qd + 16 * sub) << 16;
@@ -627,10 +585,57 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
       float* stats = reinterpret_cast<float*>(gbase + kOffStats);
       uint32_t it = 0, seg = 0;
       bool ok = true;
+      // the walk over this pair's tiles that runs ahead of the main one
+      sm100::SegIter<true> ahead = segs;
+      int ab = 0, at = 0, a_hi = 0;
+      auto next_page = [&]() -> int {   // pool page of the next tile of the walk; num_pages when it ends
+        if (at == a_hi) {
+          int lo, all;
+          if (!ahead.next(p.counts, p.rows, p.k, ab, lo, a_hi, all)) { a_hi = at; return p.num_pages; }
+          at = lo;
+        }
+        return page_at(ab, at++, false);   // a bad entry is reported by the score CTA
+      };
+      const int w8 = warp - 4, lrow = lane >> 2;
+      const uint32_t vdst = base + kOffV + (uint32_t)w8 * kBoxBytes + (uint32_t)lrow * 128u;
+      const uint32_t vsw0 = (((uint32_t)(2 * (lane & 3))) ^ (uint32_t)lrow) << 4;
+      const uint32_t vsw1 = (((uint32_t)(2 * (lane & 3) + 1)) ^ (uint32_t)lrow) << 4;
+      const uint8_t* lane_codes = p.codes + (int64_t)lrow * p.code_stride + 64 * w8 + 16 * (lane & 3);
+      uint4 cd[8];
+      auto load_codes = [&](int page) {
+        const uint8_t* src = lane_codes + (int64_t)(page < p.num_pages ? page : 0) * kTile * p.code_stride;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          cd[i] = page < p.num_pages ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(8 * i) * p.code_stride))
+                                     : make_uint4(0u, 0u, 0u, 0u);
+      };
+      load_codes(next_page());
+      int page1 = next_page();
       while (next()) {
+        const int L = vlen(b);
         for (int t = t_lo; t < t_hi; ++t, ++it) {
           if (!ok) continue;
-          const uint32_t slot = it % kPSlots;
+          const uint32_t slot = it % kPSlots, vs = it % kVStages;
+          if (!wait_bar_warp(bar(V_EMPTY + vs), ((it / kVStages) & 1u) ^ 1u, abort_addr, false)) { ok = false; continue; }
+          const int valid = L - t * kTile;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t f[8];
+            const uint32_t q[4] = {cd[i].x, cd[i].y, cd[i].z, cd[i].w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = ptx::e4m3x2_to_f16x2(q[k >> 1] >> (16 * (k & 1)));
+            if (8 * i + lrow >= valid) {   // a slot past the end may hold NaN codes, and 0 * NaN = NaN
+#pragma unroll
+              for (int k = 0; k < 8; ++k) f[k] = 0u;
+            }
+            const uint32_t dst = vdst + vs * kVStageBytes + (uint32_t)i * 1024u;
+            ptx::st_shared_v4(dst + vsw0, f[0], f[1], f[2], f[3]);
+            ptx::st_shared_v4(dst + vsw1, f[4], f[5], f[6], f[7]);
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(bar(V_FULL + vs));
+          load_codes(page1);
+          page1 = next_page();
           if (!wait_bar_warp(bar(P_FULL + slot), (it / kPSlots) & 1u, abort_addr, true)) { ok = false; continue; }
           const float* alpha_s = reinterpret_cast<const float*>(gbase + kOffPSlots + slot * kSlotStride + kAlphaOff);
           const float al0 = alpha_s[r0], al1 = alpha_s[r0 + 8];
@@ -790,6 +795,8 @@ inline int launch_decode8(const mla_dims_t* d, int32_t rows, const void* q_abs, 
   prm.counts = lists.counts;
   prm.k = lists.k;
   prm.s_q = lists.s_q;
+  prm.codes = cache->codes;
+  prm.code_stride = cache->code_stride;
   prm.scales = cache->scales;
   prm.o_lat = reinterpret_cast<__nv_bfloat16*>(o_lat);
   prm.lse = lse;
