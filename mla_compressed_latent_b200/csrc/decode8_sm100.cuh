@@ -133,8 +133,8 @@ __device__ __forceinline__ void split_e4m3x2(float w0, float w1, uint32_t* hi, u
 }
 
 // Warp roles.  Score CTA: 0 TMA producer | 1, 2 S-MMA issuers of even and odd tiles (2 owns TMEM) | 3
-// copier | 4-11 row warps. Output CTA: 1 O-MMA issuer | 2 receiver (and TMEM) | 3 rows without pages | 4-11 widening,
-// rescale and epilogue.
+// copier | 4-11 row warps. Output CTA: 0-3 rescale (1 also issues the O MMAs, 2 returns staging buffers) |
+// 4-11 widening and epilogue.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_rope,
                const __grid_constant__ CUtensorMap tm_q, const Params p) {
@@ -158,7 +158,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
     for (int i = 0; i < kPSlots; ++i) {
       ptx::mbar_init(bar(P_EMPTY + i), 1);
       ptx::mbar_init(bar(P_FULL + i), 1);
-      ptx::mbar_init(bar(P_LOCAL + i), kGroup);
+      ptx::mbar_init(bar(P_LOCAL + i), 128);
     }
     for (int i = 0; i < kStaging; ++i) { ptx::mbar_init(bar(P_WRITTEN + i), kH); ptx::mbar_init(bar(STG_FREE + i), 1); }
     ptx::mbar_init(bar(DEC_FULL), kH);
@@ -212,43 +212,52 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
   if (rank == 0) {
     // ============================== score CTA ==============================
     if (warp == 0) {
-      if (lane == 0) {   // ---- TMA producer
-        uint32_t it = 0, seg = 0;
-        bool ok = true, q_out = false;
-        while (ok && next()) {
-          // the row's query passes through the tile ring once every earlier tile's products are done
-          for (uint32_t i = (it > (uint32_t)kKStages ? it - kKStages : 0); i < it && ok; ++i)
-            ok = wait_bar(bar(K_EMPTY + i % kKStages), (i / kKStages) & 1u, abort_addr, false);
-          if (!ok) break;
+      // ---- TMA producer: the warp looks up the pages of 32 tiles at a time and waits as a whole; lane 0
+      // issues the loads
+      uint32_t it = 0, seg = 0;
+      bool ok = true, q_out = false;
+      while (ok && next()) {
+        int pages = t_lo + lane < t_hi ? page_at(b, t_lo + lane, true) : 0;
+        // the row's query passes through the tile ring once every earlier tile's products are done
+        for (uint32_t i = (it > (uint32_t)kKStages ? it - kKStages : 0); i < it && ok; ++i)
+          ok = wait_bar_warp(bar(K_EMPTY + i % kKStages), (i / kKStages) & 1u, abort_addr, false);
+        if (!ok) break;
+        if (lane == 0) {
           ptx::mbar_arrive_expect_tx(bar(Q_LOADED), (kQBoxes + 2) * kBoxBytes);
           for (int i = 0; i < kQBoxes; ++i)
             ptx::tma_load_2d(base + kOffK + i * kBoxBytes, &tm_q, 64 * (i >> 1), b * kH + 64 * (i & 1), bar(Q_LOADED));
           for (int i = 0; i < 2; ++i)
             ptx::tma_load_2d(base + kOffQR + i * kBoxBytes, &tm_q, kDC, b * kH + 64 * i, bar(Q_LOADED));
-          q_out = true;
-          // meanwhile the first tiles into L2
-          for (int t = t_lo; t < min(t_hi, t_lo + kKStages); ++t) {
-            const int page = page_at(b, t, false);
-            for (int j = 0; j < kCodeBoxes; ++j) ptx::tma_prefetch_2d(&tm_codes, 128 * j, page * kTile);
-          }
-          if (!(ok = wait_bar(bar(Q_FULL), seg & 1u, abort_addr, false))) break;
-          q_out = false;
-          ++seg;
-          for (int t = t_lo; t < t_hi; ++t, ++it) {
-            const uint32_t s = it % kKStages;
-            const int page = page_at(b, t, true);
-            if (!(ok = wait_bar(bar(K_EMPTY + s), ((it / kKStages) & 1u) ^ 1u, abort_addr, false))) break;
+        }
+        q_out = true;
+        // meanwhile the first tiles into L2 (a box a lane)
+        const int pre = min(t_hi - t_lo, kKStages);
+        const int pre_page = __shfl_sync(0xffffffffu, pages, lane / kCodeBoxes);
+        if (lane < pre * kCodeBoxes) ptx::tma_prefetch_2d(&tm_codes, 128 * (lane % kCodeBoxes), pre_page * kTile);
+        __syncwarp();
+        if (!(ok = wait_bar_warp(bar(Q_FULL), seg & 1u, abort_addr, false))) break;
+        q_out = false;
+        ++seg;
+        for (int t = t_lo; t < t_hi; ++t, ++it) {
+          const uint32_t s = it % kKStages;
+          if (t > t_lo && ((t - t_lo) & 31) == 0) pages = t + lane < t_hi ? page_at(b, t + lane, true) : 0;
+          const int page = __shfl_sync(0xffffffffu, pages, (t - t_lo) & 31);
+          if (!(ok = wait_bar_warp(bar(K_EMPTY + s), ((it / kKStages) & 1u) ^ 1u, abort_addr, false))) break;
+          if (lane == 0) {
             const uint32_t dst = base + kOffK + s * kKStageBytes;
             ptx::mbar_arrive_expect_tx(bar(K_FULL + s), kKStageBytes + kScaleBytes);
             // (an off-the-map page takes page 0's scales: its result is undefined, its reads are not)
-            ptx::bulk_load(base + kOffScale + (it % kScaleSlots) * kScaleBytes, p.scales + (size_t)(page < p.num_pages ? page : 0) * kTile,
-                           kScaleBytes, bar(K_FULL + s));
+            ptx::bulk_load(base + kOffScale + (it % kScaleSlots) * kScaleBytes,
+                           p.scales + (size_t)(page < p.num_pages ? page : 0) * kTile, kScaleBytes, bar(K_FULL + s));
             for (int j = 0; j < kCodeBoxes; ++j)
               ptx::tma_load_2d(dst + j * kBoxBytes, &tm_codes, 128 * j, page * kTile, bar(K_FULL + s));
             ptx::tma_load_2d(dst + kCodeBoxes * kBoxBytes, &tm_rope, 0, page * kTile, bar(K_FULL + s));
           }
+          __syncwarp();
         }
-        // loads still in flight must land before the CTA may exit
+      }
+      // loads still in flight must land before the CTA may exit
+      if (lane == 0) {
         if (q_out) wait_bar(bar(Q_LOADED), seg & 1u, abort_addr, false, false);
         for (uint32_t i = (it > (uint32_t)kKStages ? it - kKStages : 0); i < it; ++i)
           wait_bar(bar(K_FULL + i % kKStages), (i / kKStages) & 1u, abort_addr, false, false);
@@ -521,27 +530,20 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
     }
   } else {
     // ============================== output CTA ==============================
-    if (warp == 2) {
-      if (lane == 0) {   // ---- receiver: as each tile lands, the score CTA may reuse that staging buffer
-        uint32_t it = 0;
-        bool ok = true;
-        while (ok && next()) {
-          for (int t = t_lo; t < t_hi; ++t, ++it) {
-            if (!(ok = wait_bar(bar(P_FULL + it % kPSlots), (it / kPSlots) & 1u, abort_addr, true))) break;
-            ptx::mbar_arrive_remote(bar(STG_FREE + it % kStaging), 0);
-          }
+    if (warp < 4) {
+      // ---- control warps: as a tile of weights lands, warp w rescales its 32 rows of O if their reference
+      // moved; warp 2 hands the staging buffer back to the score CTA; warp 1 then issues O += w · value, K = 64
+      // positions in steps of 16, N = 512 in 2 halves
+      if (warp == 3) {   // (rows that list no page attend nothing: zeros and lse = -inf)
+        for (int v = pair; v < p.rows; v += npairs) {
+          if (sm100::item_tiles<true>(p.counts, v, p.k) > 0) continue;
+          uint4* o = reinterpret_cast<uint4*>(p.o_lat + (size_t)v * kH * kDC);
+          for (int i = lane; i < kH * kDC / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+          for (int i = lane; i < kH; i += 32) p.lse[(size_t)v * kH + i] = -INFINITY;
         }
+        __syncwarp();
       }
-    } else if (warp == 3) {
-      // ---- rows that list no page attend nothing: zeros and lse = -inf
-      for (int v = pair; v < p.rows; v += npairs) {
-        if (sm100::item_tiles<true>(p.counts, v, p.k) > 0) continue;
-        uint4* o = reinterpret_cast<uint4*>(p.o_lat + (size_t)v * kH * kDC);
-        for (int i = lane; i < kH * kDC / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
-        for (int i = lane; i < kH; i += 32) p.lse[(size_t)v * kH + i] = -INFINITY;
-      }
-    } else if (warp == 1) {
-      // ---- MMA issuer: O += w · value, K = 64 positions in steps of 16, N = 512 in 2 halves
+      const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
       const uint64_t v_desc0 = ptx::smem_desc_sw128(base + kOffV, kBoxBytes, 1024);
       const uint64_t p_desc0 = ptx::smem_desc_sw128(base + kOffPSlots, 16, 1024);
       uint32_t it = 0;
@@ -549,6 +551,27 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
       while (ok && next()) {
         for (int t = t_lo; t < t_hi; ++t, ++it) {
           const uint32_t slot = it % kPSlots, s = it % kVStages;
+          if (!(ok = wait_bar_warp(bar(P_FULL + slot), (it / kPSlots) & 1u, abort_addr, true))) break;
+          if (warp == 2 && lane == 0) ptx::mbar_arrive_remote(bar(STG_FREE + it % kStaging), 0);
+          const float al = reinterpret_cast<const float*>(gbase + kOffPSlots + slot * kSlotStride + kAlphaOff)[warp * 32 + lane];
+          if (t > t_lo && __any_sync(0xffffffffu, al != 1.f)) {   // once the products of the tile before are done
+            const uint32_t pt = it - 1;
+            if (!(ok = wait_bar_warp(bar(P_EMPTY + pt % kPSlots), (pt / kPSlots) & 1u, abort_addr, false))) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kDC; c += 32) {
+              uint32_t r[32];
+              ptx::tmem_ld32(tmem + lane_off + c, r);
+              ptx::tmem_wait_ld_regs(r);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al);
+              ptx::tmem_st32(tmem + lane_off + c, r);
+            }
+            ptx::tmem_wait_st();
+          }
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(P_LOCAL + slot));
+          if (warp != 1) continue;
           if (!(ok = wait_bar_warp(bar(V_FULL + s), (it / kVStages) & 1u, abort_addr, false))) break;
           if (!(ok = wait_bar_warp(bar(P_LOCAL + slot), (it / kPSlots) & 1u, abort_addr, false))) break;
           if (ptx::elect_one()) {
@@ -568,16 +591,14 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           __syncwarp();
         }
       }
-    } else if (warp >= 4) {
-      // ---- row warps: each tile's codes widened to fp16 on their way into shared memory, rescale of the
-      // warp's 16 rows of O before a tile whose weights have a newer reference, and the segment epilogue.
+    } else {
+      // ---- row warps: each tile's codes widened to fp16 on their way into shared memory, and the segment
+      // epilogue.
       // Warp w takes latents [64 w', + 64) (w' = w - 4), eight rows at a time, 16 codes a thread: the loads
       // read whole 32-byte sectors and the stores of a warp spread over all banks. A tile's codes are
       // loaded into registers while the tile before it is widened, its page is looked up one tile
       // earlier still; the loads mostly hit L2, where the score CTA's reads have brought the rows.
       const int sub = (warp - 4) >> 2, qd = warp & 3;
-      const int r0 = 32 * qd + 16 * sub + (lane >> 2);                       // and r0 + 8
-      const uint32_t s_lane = (uint32_t)(32 * qd + 16 * sub) << 16;
       const int g = sub;                                  // epilogue: latent half g
       const int h = (qd << 5) | lane;
       const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
@@ -587,14 +608,19 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
       bool ok = true;
       // the walk over this pair's tiles that runs ahead of the main one
       sm100::SegIter<true> ahead = segs;
-      int ab = 0, at = 0, a_hi = 0;
+      int ab = 0, at = 0, a_lo = 0, a_hi = 0, a_pages = 0;   // lane l: page of the l-th tile of the current 32
       auto next_page = [&]() -> int {   // pool page of the next tile of the walk; num_pages when it ends
+        bool fresh = at < a_hi && ((at - a_lo) & 31) == 0;
         if (at == a_hi) {
-          int lo, all;
-          if (!ahead.next(p.counts, p.rows, p.k, ab, lo, a_hi, all)) { a_hi = at; return p.num_pages; }
-          at = lo;
+          int all;
+          if (!ahead.next(p.counts, p.rows, p.k, ab, a_lo, a_hi, all)) { a_hi = at; return p.num_pages; }
+          at = a_lo;
+          fresh = true;
         }
-        return page_at(ab, at++, false);   // a bad entry is reported by the score CTA
+        if (fresh) a_pages = at + lane < a_hi ? page_at(ab, at + lane, false) : 0;   // (the score CTA reports)
+        const int page = __shfl_sync(0xffffffffu, a_pages, (at - a_lo) & 31);
+        ++at;
+        return page;
       };
       const int w8 = warp - 4, lrow = lane >> 2;
       const uint32_t vdst = base + kOffV + (uint32_t)w8 * kBoxBytes + (uint32_t)lrow * 128u;
@@ -615,7 +641,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
         const int L = vlen(b);
         for (int t = t_lo; t < t_hi; ++t, ++it) {
           if (!ok) continue;
-          const uint32_t slot = it % kPSlots, vs = it % kVStages;
+          const uint32_t vs = it % kVStages;
           if (!wait_bar_warp(bar(V_EMPTY + vs), ((it / kVStages) & 1u) ^ 1u, abort_addr, false)) { ok = false; continue; }
           const int valid = L - t * kTile;
 #pragma unroll
@@ -636,31 +662,6 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           ptx::mbar_arrive(bar(V_FULL + vs));
           load_codes(page1);
           page1 = next_page();
-          if (!wait_bar_warp(bar(P_FULL + slot), (it / kPSlots) & 1u, abort_addr, true)) { ok = false; continue; }
-          const float* alpha_s = reinterpret_cast<const float*>(gbase + kOffPSlots + slot * kSlotStride + kAlphaOff);
-          const float al0 = alpha_s[r0], al1 = alpha_s[r0 + 8];
-          if (t > t_lo && __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
-            const uint32_t pt = it - 1;
-            if (!wait_bar_warp(bar(P_EMPTY + pt % kPSlots), (pt / kPSlots) & 1u, abort_addr, false)) { ok = false; continue; }
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < kDC; c += 64) {
-              uint32_t r[32];
-              ptx::tmem_ld_16x256b_x8(tmem + s_lane + c, r);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) * al0);
-                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) * al0);
-                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) * al1);
-                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) * al1);
-              }
-              ptx::tmem_st_16x256b_x8(tmem + s_lane + c, r);
-            }
-            ptx::tmem_wait_st();
-          }
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(P_LOCAL + slot));
         }
         if (ok && !wait_bar_warp(bar(P_EMPTY + (it - 1) % kPSlots), ((it - 1) / kPSlots) & 1u, abort_addr, false)) ok = false;
         if (ok && !wait_bar_warp(bar(STATS_FULL), seg & 1u, abort_addr, true)) ok = false;
@@ -717,6 +718,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
             flush(reinterpret_cast<char*>(dst), kDC * sizeof(__nv_bfloat16));
           }
         }
+        // (the next segment's first product overwrites O: it waits for these threads' next tile)
         ptx::tc_fence_before();
         ptx::mbar_arrive_remote(bar(STATS_EMPTY), 0);
         ++seg;
