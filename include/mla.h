@@ -331,7 +331,8 @@ MLA_API int mla_decode_absorbed_fp8(const mla_dims_t* dims, int32_t dtype, int32
  *   codes) and k_r in the RoPE row. c is quantised from its fp32 value: it is not rounded to dtype
  *   first, as mla_append_cache followed by mla_quantize_latent_fp8 would. The call WRITES the arrays
  *   the descriptor names. d_c must be a multiple of 16 (else MLA_ERR_UNSUPPORTED). Other arguments,
- *   layouts, the workspace (mla_append_workspace_size) and errors are those of mla_append_cache.
+ *   layouts and errors are those of mla_append_cache; workspace: at least
+ *   mla_append_fp8_workspace_size(...) bytes, no initialisation needed.
  *   A position given twice in one call (two tokens that map to one cache row) is the caller's error:
  *   which row is stored is then undefined.
  * mla_read_latent_fp8: rows of the cache in storage type. Output row r, row_offsets[b] <= r <
@@ -342,6 +343,7 @@ MLA_API int mla_decode_absorbed_fp8(const mla_dims_t* dims, int32_t dtype, int32
  *   n_rows write nothing past it. A position outside the table row or a page id outside the pool is
  *   reported (MLA_ERR_DEVICE_CHECK) and its output row left as it was. d_c a multiple of 16.
  * ------------------------------------------------------------------------------------------- */
+MLA_API size_t mla_append_fp8_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, int32_t C);
 MLA_API int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* x, int32_t C,
                                  const void* w_dkv_kr, const void* gamma, const int32_t* seqlens,
                                  const int32_t* block_table, int32_t max_pages, const mla_latent_cache_fp8_t* cache,

@@ -81,6 +81,7 @@ SIGNATURES = {
     "mla_decode_fp8_workspace_size": (c_size_t, [PD, c_int32, c_int32, c_int32]),
     "mla_decode_absorbed_fp8": (c_int32, [PD, c_int32, c_int32, c_int32, c_void_p, POINTER(MlaLatentCacheFp8), PI,
                                           c_int32, PI, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "mla_append_fp8_workspace_size": (c_size_t, [PD, c_int32, c_int32, c_int32, c_int32]),
     "mla_append_cache_fp8": (c_int32, [PD, c_int32, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p, PI, PI,
                                        c_int32, POINTER(MlaLatentCacheFp8), c_void_p, c_size_t, c_void_p]),
     "mla_read_latent_fp8": (c_int32, [PD, c_int32, c_int32, POINTER(MlaLatentCacheFp8), PI, c_int32, PI, PI, c_int64,

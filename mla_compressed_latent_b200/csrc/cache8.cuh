@@ -81,6 +81,104 @@ __global__ void append_fp8_finish_kernel(const float* __restrict__ part, int ksp
   simt::finish_rope(z + d_c, d_r / 2, groups > 0 ? cs_sn : nullptr, s_pos, d_r, rope_base, rope + row * rope_stride);
 }
 
+// The same for many tokens (few K slices each): a warp per token, the whole row in registers, so that
+// no block waits between the sums, the norm, the scale and the stores; the rotation's frequencies are made
+// once per block. d_c % 16 == 0, (d_c + d_r) % 4 == 0, d_c <= 128 * kRowChunks, d_r <= 64 * kRowPairs, 16-byte
+// aligned slices. For 4096 tokens of 512 + 64 values in one slice: 104 us for a block a token, 9 us so.
+constexpr int kRowChunks = 8;     // float4 pieces of the latent row a lane may hold
+constexpr int kRowPairs = 4;      // rotated pairs a lane may hold
+constexpr int kRowWarps = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowWarps)
+append_fp8_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, int s_q, int d_c, int d_r,
+                       const T* __restrict__ gamma, float eps, float rope_base, const int32_t* __restrict__ seqlens,
+                       const int32_t* __restrict__ block_table, int max_pages, uint8_t* codes, int64_t code_stride,
+                       float* scales, T* rope, int64_t rope_stride, int num_pages) {
+  __shared__ double inv_freq[32 * kRowPairs];
+  for (int i = threadIdx.x; i < d_r / 2; i += blockDim.x) inv_freq[i] = rope_inv_freq(i, d_r, rope_base);
+  __syncthreads();
+  grid_dependency_wait();
+  allow_dependents();
+  const int lane = threadIdx.x & 31;
+  const int tok = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (tok >= n_tok) return;
+  const int b = tok / s_q, pos = seqlens[b] - s_q + tok % s_q;
+  int64_t row = -1;
+  if (pos < 0 || (pos >> 6) >= max_pages) {
+    if (lane == 0) report(MLA_ERR_DEVICE_CHECK);
+  } else {
+    const int page = block_table[(int64_t)b * max_pages + (pos >> 6)];
+    if (page >= 0 && page < num_pages) row = (int64_t)page * 64 + (pos & 63);
+    else if (lane == 0) report(MLA_ERR_DEVICE_CHECK);
+  }
+  if (row < 0) return;
+  const int N = d_c + d_r, chunks = d_c / 4;
+  const float* src = part + (int64_t)tok * N;
+  const int64_t step = (int64_t)n_tok * N;   // one slice
+  float4 z[kRowChunks];
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < kRowChunks; ++j) {
+    const int c = lane + 32 * j;
+    z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < chunks) {
+      for (int s = 0; s < ksplit; ++s) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + s * step) + c);
+        z[j].x += v.x; z[j].y += v.y; z[j].z += v.z; z[j].w += v.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRowChunks; ++j)
+    ss += fmaf(z[j].x, z[j].x, z[j].y * z[j].y) + fmaf(z[j].z, z[j].z, z[j].w * z[j].w);
+  ss = warp_sum(ss);
+  const float inv = 1.0f / sqrtf(ss / (float)d_c + eps);
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < kRowChunks; ++j) {
+    const int c = lane + 32 * j;
+    if (c < chunks) {
+      z[j].x *= inv; z[j].y *= inv; z[j].z *= inv; z[j].w *= inv;
+      if (gamma) {
+        z[j].x *= ld(gamma + 4 * c); z[j].y *= ld(gamma + 4 * c + 1);
+        z[j].z *= ld(gamma + 4 * c + 2); z[j].w *= ld(gamma + 4 * c + 3);
+      }
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(z[j].x), fabsf(z[j].y)), fmaxf(fabsf(z[j].z), fabsf(z[j].w))));
+    }
+  }
+  amax = warp_max(amax);
+  const float s = __fdiv_rn(amax, 448.f);
+  const float safe = s > 0.f ? s : 1.f;
+  uint8_t* dst = codes + row * code_stride;
+#pragma unroll
+  for (int j = 0; j < kRowChunks; ++j) {
+    const int c = lane + 32 * j;
+    if (c < chunks) {
+      const float v[4] = {z[j].x, z[j].y, z[j].z, z[j].w};
+      *reinterpret_cast<uint32_t*>(dst + 4 * c) = e4m3x4_codes(v, safe);
+    }
+  }
+  if (lane == 0) scales[row] = s;
+  T* krow = rope + row * rope_stride;
+#pragma unroll
+  for (int j = 0; j < kRowPairs; ++j) {
+    const int i = lane + 32 * j;
+    if (i < d_r / 2) {
+      float a = 0.f, bb = 0.f;
+      for (int sl = 0; sl < ksplit; ++sl) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(src + sl * step + d_c) + i);
+        a += v.x;
+        bb += v.y;
+      }
+      float cs, sn;
+      rope_cos_sin_at(pos, inv_freq[i], &cs, &sn);
+      st(krow + 2 * i, a * cs - bb * sn);
+      st(krow + 2 * i + 1, a * sn + bb * cs);
+    }
+  }
+}
+
 // =============================================================================================
 // Read back: out row r (row_offsets[b] <= r < row_offsets[b + 1]) = [s · value(code) ; k_r] of position
 // first[b] + r - row_offsets[b] of sequence b. Bound by its bytes: d_c + 4 + d_r·e in, (d_c + d_r)·e out

@@ -147,6 +147,21 @@ SimtSplit simt_split(int n_tok, int H, int max_pages) {
   return {ns, chunk};
 }
 
+// The same for lists of k pages. They are short: a block per tile of 32 positions, where that takes, makes the
+// launch a single wave of one tile each (fp32, 4 rows x 16 pages: 115 us with splits of 256 positions).
+SimtSplit sparse_split(int n_tok, int H, int k) {
+  const int64_t len = (int64_t)k * 64;
+  const int64_t base = (int64_t)n_tok * (H / mla::simt::DEC_HEADS);
+  const int64_t ns = std::max<int64_t>(1, std::min<int64_t>(64, (2 * num_sms() + base - 1) / base));
+  const int64_t chunk = ((len + ns - 1) / ns + 31) / 32 * 32;
+  return {(int)((len + chunk - 1) / chunk), (int)chunk};
+}
+size_t split_ws(SimtSplit s, int n_tok, int H, int Dv) {
+  if (s.nsplit <= 1) return 0;
+  const size_t slots = (size_t)n_tok * H * s.nsplit;
+  return slots * Dv * sizeof(float) + slots * sizeof(float) + 256;
+}
+
 size_t simt_decode_ws(int n_tok, int H, int Dv, int max_pages) {
   SimtSplit s = simt_split(n_tok, H, max_pages);
   if (s.nsplit <= 1) return 0;
@@ -710,6 +725,35 @@ int latent_cache_args(const mla_dims_t* dims, int32_t dtype, const mla_latent_ca
 }
 }  // namespace
 
+namespace {
+// How the 8-bit append projects: a wide tile (three 128-feature tiles per CTA) for token counts whose blocks
+// of 128 fill a good part of the SMs, K cut so that the rest is filled; else the split of a1.
+struct AppendPlan {
+  bool tc, wide;
+  int ks;
+};
+constexpr int kWideTokens = 512;   // tokens from which the wide tile is taken
+AppendPlan append_fp8_plan(int32_t dtype, int n_tok, int C, int N) {
+  AppendPlan a{append_on_tc(dtype, C, N), false, 0};
+  a.wide = a.tc && n_tok >= kWideTokens;
+  if (a.wide) {
+    const int ctas = ((N + 127) / 128 + 2) / 3 * ((n_tok + 127) / 128), chunks = C / mla::gemm::kBK;
+    const int ks = std::max(1, std::min(num_sms() / ctas, chunks));
+    const int per = (chunks + ks - 1) / ks;
+    a.ks = (chunks + per - 1) / per;
+  } else {
+    a.ks = a.tc ? append_tc_splits(n_tok, C, N) : append_ksplit(n_tok, C, N);
+  }
+  return a;
+}
+}  // namespace
+
+size_t mla_append_fp8_workspace_size(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, int32_t C) {
+  if (check_dims(dims) || check_dtype(dtype) || !tokens_ok(B, s_q) || C <= 0) return 0;
+  const int n_tok = B * s_q, N = dims->d_c + dims->d_r;
+  return (size_t)append_fp8_plan(dtype, n_tok, C, N).ks * n_tok * N * sizeof(float);
+}
+
 int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* x, int32_t C,
                          const void* w_dkv_kr, const void* gamma, const int32_t* seqlens, const int32_t* block_table,
                          int32_t max_pages, const mla_latent_cache_fp8_t* cache, void* workspace, size_t ws_bytes,
@@ -725,8 +769,9 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
   if ((rc = fp8_cache_args(dims, dtype, cache))) return rc;
   if (dims->d_c % 16) return MLA_ERR_UNSUPPORTED;
   const int n_tok = B * s_q, N = dims->d_c + dims->d_r;
-  const bool tc = append_on_tc(dtype, C, N);
-  const int ks = tc ? append_tc_splits(n_tok, C, N) : append_ksplit(n_tok, C, N);
+  const AppendPlan plan = append_fp8_plan(dtype, n_tok, C, N);
+  const bool tc = plan.tc;
+  const int ks = plan.ks;
   if (!workspace || ws_bytes < (size_t)ks * n_tok * N * sizeof(float)) return MLA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -736,6 +781,9 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
                              : set_smem(mla::cache8::append_fp8_finish_kernel<__nv_bfloat16>, fs.smem)))
     return rc;
   float* part = reinterpret_cast<float*>(workspace);
+  // with few slices a row a warp is as quick to sum as to spread over a block, and there are rows enough
+  const bool rows_in_warps = ks <= 8 && n_tok >= 2 * num_sms() && N % 4 == 0 && dims->d_c <= 128 * mla::cache8::kRowChunks &&
+                             dims->d_r <= 64 * mla::cache8::kRowPairs;
   auto run = [&](auto zero) -> int {
     using T = decltype(zero);
     if (tc) {
@@ -743,13 +791,23 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
       p.mode = 1;
       p.part = part;
       p.w_early = 1;
-      if (int e = mla::gemm::run(with_sms({w_dkv_kr, x, 1, C, N, n_tok, ks}), p, st)) return e;
+      mla::gemm::Problem pr = with_sms({w_dkv_kr, x, 1, C, N, n_tok, ks});
+      if (plan.wide) pr.m_per_cta = 3;
+      if (int e = mla::gemm::run(pr, p, st)) return e;
     } else {
       const int k_chunk = ((C + ks - 1) / ks + 63) / 64 * 64;
       dim3 grid((N + mla::simt::PROJ_COLS - 1) / mla::simt::PROJ_COLS,
                 (n_tok + mla::simt::PROJ_TOK - 1) / mla::simt::PROJ_TOK, ks);
       launch(mla::simt::proj_partial_kernel<T>, grid, mla::simt::PROJ_COLS, 0, st, (const T*)x, n_tok, C,
              (const T*)w_dkv_kr, N, k_chunk, part, (T*)nullptr);
+    }
+    if (rows_in_warps) {
+      mla::launch_pdl(mla::cache8::append_fp8_rows_kernel<T>, dim3((n_tok + mla::cache8::kRowWarps - 1) / mla::cache8::kRowWarps),
+                      dim3(32 * mla::cache8::kRowWarps), 0, st, (const float*)part, ks, n_tok, s_q, dims->d_c, dims->d_r,
+                      (const T*)gamma, dims->rms_eps, dims->rope_base, seqlens, block_table, max_pages,
+                      const_cast<uint8_t*>(cache->codes), cache->code_stride, const_cast<float*>(cache->scales),
+                      (T*)const_cast<void*>(cache->rope), cache->rope_stride, cache->num_pages);
+      return launch_status();
     }
     mla::launch_pdl(mla::cache8::append_fp8_finish_kernel<T>, dim3(n_tok), dim3(fs.threads), fs.smem, st,
                     (const float*)part, ks, n_tok, s_q, dims->d_c, dims->d_r, (const T*)gamma, dims->rms_eps,
@@ -931,10 +989,17 @@ int sparse_simt(const mla_dims_t* dims, int32_t dtype, DecodeArgs A, int32_t B, 
   A.seqlens = seqlens; A.s_q = s_q; A.sm_scale = score_scale(dims); A.rope_base = dims->rope_base;
   A.out = o_lat; A.out_head_stride = dims->d_c; A.lse = lse;
   A.page_list = pages; A.counts = counts; A.list_k = k;
-  SimtSplit sp = simt_split(n_tok, dims->H, k);
+  SimtSplit sp = sparse_split(n_tok, dims->H, k);
   A.nsplit = sp.nsplit; A.chunk = sp.chunk;
   return dtype == MLA_F32 ? launch_decode_simt<float>(A, n_tok, workspace, ws_bytes, st)
                           : launch_decode_simt<__nv_bfloat16>(A, n_tok, workspace, ws_bytes, st);
+}
+}  // namespace
+
+namespace {
+size_t sparse_ws(const mla_dims_t* dims, int rows, int k) {
+  if (dims->H < mla::simt::DEC_HEADS || k > INT32_MAX / 64) return 0;   // (shapes the call refuses)
+  return split_ws(sparse_split(rows, dims->H, k), rows, dims->H, dims->d_c);
 }
 }  // namespace
 
@@ -942,7 +1007,7 @@ size_t mla_decode_sparse_workspace_size(const mla_dims_t* dims, int32_t dtype, i
   if (check_dims(dims) || check_dtype(dtype) || !tokens_ok(B, s_q) || k <= 0) return 0;
   if (mla::sm100::decode_supported(dims, dtype, B * s_q, 1))
     return mla::sm100::decode_workspace_bytes(dims, dtype, B * s_q, 1, num_sms());
-  return simt_decode_ws(B * s_q, dims->H, dims->d_c, k);
+  return sparse_ws(dims, B * s_q, k);
 }
 
 int mla_decode_absorbed_sparse(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* q_abs,
@@ -971,7 +1036,7 @@ size_t mla_decode_sparse_fp8_workspace_size(const mla_dims_t* dims, int32_t dtyp
   if (check_dims(dims) || check_dtype(dtype) || !tokens_ok(B, s_q) || k <= 0) return 0;
   if (mla::sm100::decode_supported(dims, dtype, B * s_q, 1))
     return mla::sm100::decode_workspace_bytes(dims, dtype, B * s_q, 1, num_sms());
-  return simt_decode_ws(B * s_q, dims->H, dims->d_c, k);
+  return sparse_ws(dims, B * s_q, k);
 }
 
 int mla_decode_absorbed_sparse_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32_t s_q, const void* q_abs,

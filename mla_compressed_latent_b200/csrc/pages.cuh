@@ -67,7 +67,7 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, float sc, float (&f
 }
 
 constexpr int kKeyGroups = 8;
-constexpr int kKeyThreads = 768;   // most threads of a block
+constexpr int kKeyThreads = 640;   // most threads of a block
 
 // V: columns per piece (16 bytes of T, or 1 when a width is not a multiple of that); kCodes: 8-bit rows.
 template <typename T, int V, bool kCodes>
@@ -97,19 +97,26 @@ page_keys_kernel(CacheView<T> cache, const int32_t* __restrict__ block_table, in
   const int W = d_c + d_r, Q = W / V, qc = d_c / V;
   for (int it = threadIdx.x; it < Q * kKeyGroups; it += blockDim.x) {
     const int q = it % Q, g = it / Q;
+    // all of the thread's rows are loaded before the first is added
+    float f[64 / kKeyGroups][V];
+#pragma unroll
+    for (int u = 0; u < 64 / kKeyGroups; ++u) {
+      const int r = g + u * kKeyGroups;
+      const int64_t row = (int64_t)page * 64 + r;
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[u][k] = 0.f;
+      if (r >= n) continue;
+      if (q >= qc) load_vec<T, V>(cache.rope + row * cache.rope_stride + (q - qc) * V, f[u]);
+      else if constexpr (kCodes) load_codes<V>(cache.codes + row * cache.code_stride + q * V, cache.scales[row], f[u]);
+      else load_vec<T, V>(cache.latent + row * cache.latent_stride + q * V, f[u]);
+    }
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
-#pragma unroll 8
-    for (int r = g; r < n; r += kKeyGroups) {
-      const int64_t row = (int64_t)page * 64 + r;
-      float f[V];
-      if (q >= qc) load_vec<T, V>(cache.rope + row * cache.rope_stride + (q - qc) * V, f);
-      else if constexpr (kCodes) load_codes<V>(cache.codes + row * cache.code_stride + q * V, cache.scales[row], f);
-      else load_vec<T, V>(cache.latent + row * cache.latent_stride + q * V, f);
 #pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] += f[k];
-    }
+    for (int u = 0; u < 64 / kKeyGroups; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] += f[u][k];
 #pragma unroll
     for (int k = 0; k < V; ++k) part[g * W + q * V + k] = acc[k];
   }

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + kOffSlot + 8);
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) { ptx::mbar_init(bar(FULL + i), kWorkers); ptx::mbar_init(bar(EMPTY + i), 1); }
+    for (int i = 0; i < kStages; ++i) { ptx::mbar_init(bar(FULL + i), kWorkers / 32); ptx::mbar_init(bar(EMPTY + i), 1); }
     for (int i = 0; i < kMaxChunks; ++i) ptx::mbar_init(bar(Q_FULL + i), 1);
     ptx::mbar_init(bar(DONE), 1);
     *abort = 0;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
           next1 = page_of((tile + 1) * kTile + r0 + 32);
         }
         const int s = i % kStages;
-        if (i >= kStages) live = gemm::wait(bar(EMPTY + s), ((i / kStages) & 1u) ^ 1u, abort);
+        if (i >= kStages) live = __all_sync(0xffffffffu, gemm::wait(bar(EMPTY + s), ((i / kStages) & 1u) ^ 1u, abort));
         if (live) {
           const int col = kc * 64 + piece * 8;
           const bool in = col < p.W;
@@ -138,10 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
         if (++kc == chunks) { kc = 0; ++tile; }
       }
       cp_async_commit();
-      if (i >= kAhead && live) {   // this thread's copies of stage i - kAhead have landed: hand it over
+      if (i >= kAhead && live) {   // this warp's copies of stage i - kAhead have landed: hand it over
         cp_async_wait<kAhead>();
         ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(bar(FULL + (i - kAhead) % kStages));
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(FULL + (i - kAhead) % kStages));
       }
     }
     cp_async_wait<0>();

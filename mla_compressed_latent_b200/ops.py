@@ -373,7 +373,7 @@ def mla_append_cache_fp8(dims: Dims, x, w_dkv_kr, gamma, seqlens, block_table, c
     table, max_pages, lens = _table(dev, B, block_table, seqlens)
     cc = _cache_arg(dev, dims, cache, x.dtype)
     d = dims.c()
-    need = lib.mla_append_workspace_size(ctypes.byref(d), B, s_q, C)
+    need = lib.mla_append_fp8_workspace_size(ctypes.byref(d), dt, B, s_q, C)
     workspace, ws, wsb = _space(dev, need, workspace)
     rc = lib.mla_append_cache_fp8(ctypes.byref(d), dt, B, s_q, px, C, pw, pg, lens, table, max_pages, ctypes.byref(cc),
                                   ws, wsb, _stream_on(dev, stream))

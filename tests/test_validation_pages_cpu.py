@@ -162,7 +162,7 @@ def test_sparse_decode_refuses_shapes_without_a_kernel(lib):
 
 def test_size_queries_answer_zero_for_bad_arguments(lib):
     d = _dims()
-    for fn in (lib.mla_score_pages_workspace_size, lib.mla_decode_sparse_workspace_size,
+    for fn in (lib.mla_append_fp8_workspace_size, lib.mla_score_pages_workspace_size, lib.mla_decode_sparse_workspace_size,
                lib.mla_decode_sparse_fp8_workspace_size):
         for args in [(7, 1, 1, 16), (1, 0, 1, 16), (1, 1, 0, 16), (1, 1, 1, 0), (1, 1 << 16, 1 << 16, 16)]:
             assert fn(ctypes.byref(d), *args) == 0
