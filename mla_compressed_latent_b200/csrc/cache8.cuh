@@ -101,80 +101,83 @@ append_fp8_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, in
   grid_dependency_wait();
   allow_dependents();
   const int lane = threadIdx.x & 31;
-  const int tok = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  if (tok >= n_tok) return;
-  const int b = tok / s_q, pos = seqlens[b] - s_q + tok % s_q;
-  int64_t row = -1;
-  if (pos < 0 || (pos >> 6) >= max_pages) {
-    if (lane == 0) report(MLA_ERR_DEVICE_CHECK);
-  } else {
-    const int page = block_table[(int64_t)b * max_pages + (pos >> 6)];
-    if (page >= 0 && page < num_pages) row = (int64_t)page * 64 + (pos & 63);
-    else if (lane == 0) report(MLA_ERR_DEVICE_CHECK);
-  }
-  if (row < 0) return;
   const int N = d_c + d_r, chunks = d_c / 4;
-  const float* src = part + (int64_t)tok * N;
   const int64_t step = (int64_t)n_tok * N;   // one slice
-  float4 z[kRowChunks];
-  float ss = 0.f;
+  for (int tok = blockIdx.x * kRowWarps + (threadIdx.x >> 5); tok < n_tok; tok += gridDim.x * kRowWarps) {
+    const int b = tok / s_q, pos = seqlens[b] - s_q + tok % s_q;
+    int64_t row = -1;
+    if (pos < 0 || (pos >> 6) >= max_pages) {
+      if (lane == 0) report(MLA_ERR_DEVICE_CHECK);
+    } else {
+      const int page = block_table[(int64_t)b * max_pages + (pos >> 6)];
+      if (page >= 0 && page < num_pages) row = (int64_t)page * 64 + (pos & 63);
+      else if (lane == 0) report(MLA_ERR_DEVICE_CHECK);
+    }
+    if (row < 0) continue;
+    const float* src = part + (int64_t)tok * N;
+    float4 z[kRowChunks];
+    float2 zr[kRowPairs];
 #pragma unroll
-  for (int j = 0; j < kRowChunks; ++j) {
-    const int c = lane + 32 * j;
-    z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < chunks) {
-      for (int s = 0; s < ksplit; ++s) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + s * step) + c);
-        z[j].x += v.x; z[j].y += v.y; z[j].z += v.z; z[j].w += v.w;
+    for (int j = 0; j < kRowChunks; ++j) z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kRowPairs; ++j) zr[j] = make_float2(0.f, 0.f);
+    for (int s = 0; s < ksplit; ++s) {   // a slice's loads all in flight
+      const float* sl = src + s * step;
+      float4 v[kRowChunks];
+      float2 r[kRowPairs];
+#pragma unroll
+      for (int j = 0; j < kRowChunks; ++j)
+        v[j] = lane + 32 * j < chunks ? __ldcg(reinterpret_cast<const float4*>(sl) + lane + 32 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kRowPairs; ++j)
+        r[j] = lane + 32 * j < d_r / 2 ? __ldcg(reinterpret_cast<const float2*>(sl + d_c) + lane + 32 * j) : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kRowChunks; ++j) { z[j].x += v[j].x; z[j].y += v[j].y; z[j].z += v[j].z; z[j].w += v[j].w; }
+#pragma unroll
+      for (int j = 0; j < kRowPairs; ++j) { zr[j].x += r[j].x; zr[j].y += r[j].y; }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < kRowChunks; ++j)
+      ss += fmaf(z[j].x, z[j].x, z[j].y * z[j].y) + fmaf(z[j].z, z[j].z, z[j].w * z[j].w);
+    ss = warp_sum(ss);
+    const float inv = 1.0f / sqrtf(ss / (float)d_c + eps);
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < kRowChunks; ++j) {
+      const int c = lane + 32 * j;
+      if (c < chunks) {
+        z[j].x *= inv; z[j].y *= inv; z[j].z *= inv; z[j].w *= inv;
+        if (gamma) {
+          z[j].x *= ld(gamma + 4 * c); z[j].y *= ld(gamma + 4 * c + 1);
+          z[j].z *= ld(gamma + 4 * c + 2); z[j].w *= ld(gamma + 4 * c + 3);
+        }
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(z[j].x), fabsf(z[j].y)), fmaxf(fabsf(z[j].z), fabsf(z[j].w))));
       }
     }
-  }
+    amax = warp_max(amax);
+    const float s = __fdiv_rn(amax, 448.f);
+    const float safe = s > 0.f ? s : 1.f;
+    uint8_t* dst = codes + row * code_stride;
 #pragma unroll
-  for (int j = 0; j < kRowChunks; ++j)
-    ss += fmaf(z[j].x, z[j].x, z[j].y * z[j].y) + fmaf(z[j].z, z[j].z, z[j].w * z[j].w);
-  ss = warp_sum(ss);
-  const float inv = 1.0f / sqrtf(ss / (float)d_c + eps);
-  float amax = 0.f;
-#pragma unroll
-  for (int j = 0; j < kRowChunks; ++j) {
-    const int c = lane + 32 * j;
-    if (c < chunks) {
-      z[j].x *= inv; z[j].y *= inv; z[j].z *= inv; z[j].w *= inv;
-      if (gamma) {
-        z[j].x *= ld(gamma + 4 * c); z[j].y *= ld(gamma + 4 * c + 1);
-        z[j].z *= ld(gamma + 4 * c + 2); z[j].w *= ld(gamma + 4 * c + 3);
+    for (int j = 0; j < kRowChunks; ++j) {
+      const int c = lane + 32 * j;
+      if (c < chunks) {
+        const float v[4] = {z[j].x, z[j].y, z[j].z, z[j].w};
+        *reinterpret_cast<uint32_t*>(dst + 4 * c) = e4m3x4_codes(v, safe);
       }
-      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(z[j].x), fabsf(z[j].y)), fmaxf(fabsf(z[j].z), fabsf(z[j].w))));
     }
-  }
-  amax = warp_max(amax);
-  const float s = __fdiv_rn(amax, 448.f);
-  const float safe = s > 0.f ? s : 1.f;
-  uint8_t* dst = codes + row * code_stride;
+    if (lane == 0) scales[row] = s;
+    T* krow = rope + row * rope_stride;
 #pragma unroll
-  for (int j = 0; j < kRowChunks; ++j) {
-    const int c = lane + 32 * j;
-    if (c < chunks) {
-      const float v[4] = {z[j].x, z[j].y, z[j].z, z[j].w};
-      *reinterpret_cast<uint32_t*>(dst + 4 * c) = e4m3x4_codes(v, safe);
-    }
-  }
-  if (lane == 0) scales[row] = s;
-  T* krow = rope + row * rope_stride;
-#pragma unroll
-  for (int j = 0; j < kRowPairs; ++j) {
-    const int i = lane + 32 * j;
-    if (i < d_r / 2) {
-      float a = 0.f, bb = 0.f;
-      for (int sl = 0; sl < ksplit; ++sl) {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(src + sl * step + d_c) + i);
-        a += v.x;
-        bb += v.y;
+    for (int j = 0; j < kRowPairs; ++j) {
+      const int i = lane + 32 * j;
+      if (i < d_r / 2) {
+        float cs, sn;
+        rope_cos_sin_at(pos, inv_freq[i], &cs, &sn);
+        st(krow + 2 * i, zr[j].x * cs - zr[j].y * sn);
+        st(krow + 2 * i + 1, zr[j].x * sn + zr[j].y * cs);
       }
-      float cs, sn;
-      rope_cos_sin_at(pos, inv_freq[i], &cs, &sn);
-      st(krow + 2 * i, a * cs - bb * sn);
-      st(krow + 2 * i + 1, a * sn + bb * cs);
     }
   }
 }
@@ -182,7 +185,7 @@ append_fp8_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, in
 // =============================================================================================
 // Read back: out row r (row_offsets[b] <= r < row_offsets[b + 1]) = [s · value(code) ; k_r] of position
 // first[b] + r - row_offsets[b] of sequence b. Bound by its bytes: d_c + 4 + d_r·e in, (d_c + d_r)·e out
-// per row. A block takes kReadRows consecutive rows: one warp finds the sequence of the first by a
+// per row. A block takes up to kReadRows consecutive rows: one warp finds the sequence of the first by a
 // 32-way search of row_offsets, a thread per row walks on from there and looks its cache row up, and
 // then all threads move 16 codes each at a time.
 // =============================================================================================
@@ -194,13 +197,13 @@ __global__ void __launch_bounds__(kReadThreads)
 read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const float* __restrict__ scales,
                 const T* __restrict__ rope, int64_t rope_stride, int num_pages, const int32_t* __restrict__ block_table,
                 int max_pages, const int32_t* __restrict__ first, const int32_t* __restrict__ row_offsets, int B,
-                int64_t n_rows, int d_c, int d_r, T* __restrict__ out, int64_t out_stride) {
+                int64_t n_rows, int rows_per_block, int d_c, int d_r, T* __restrict__ out, int64_t out_stride) {
   __shared__ int64_t src_row[kReadRows];   // -1: nothing to write there
   __shared__ float src_scale[kReadRows];
   __shared__ int s_b;
   grid_dependency_wait();
   allow_dependents();
-  const int64_t r0 = (int64_t)blockIdx.x * kReadRows;
+  const int64_t r0 = (int64_t)blockIdx.x * rows_per_block;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     // the last b in [0, B] with row_offsets[b] <= r0: each step keeps the one of 32 pieces that holds it
@@ -216,11 +219,15 @@ read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const fl
     if (lane == 0) s_b = lo;
   }
   __syncthreads();
-  if (threadIdx.x < kReadRows) {
+  if ((int)threadIdx.x < rows_per_block) {
     const int64_t r = r0 + threadIdx.x;
     int64_t row = -1;
-    int b = s_b;
-    while (b < B && r >= (int64_t)row_offsets[b + 1]) ++b;
+    // the last b >= s_b with row_offsets[b] <= r: steps that double, then halve (short sequences may put
+    // every row of the block in another one)
+    int b = s_b, stride = 1;
+    while (b + stride <= B && (int64_t)row_offsets[b + stride] <= r) { b += stride; stride *= 2; }
+    for (; stride > 0; stride >>= 1)
+      if (b + stride <= B && (int64_t)row_offsets[b + stride] <= r) b += stride;
     if (r < n_rows && b < B) {
       const int64_t p = (int64_t)(first ? first[b] : 0) + (r - row_offsets[b]);
       if (r < row_offsets[b] || p < 0 || (p >> 6) >= max_pages) report(MLA_ERR_DEVICE_CHECK);
@@ -232,7 +239,7 @@ read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const fl
   __syncthreads();
   const int pieces = d_c / 16;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < kReadRows * pieces; i += kReadThreads) {
+  for (int i = threadIdx.x; i < rows_per_block * pieces; i += kReadThreads) {
     const int r = i / pieces, c = i % pieces;
     const int64_t row = src_row[r];
     if (row < 0) continue;
@@ -255,7 +262,7 @@ read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const fl
   constexpr int E = 16 / (int)sizeof(T);
   if (d_r % E == 0) {
     const int rp = d_r / E;
-    for (int i = threadIdx.x; i < kReadRows * rp; i += kReadThreads) {
+    for (int i = threadIdx.x; i < rows_per_block * rp; i += kReadThreads) {
       const int r = i / rp, c = i % rp;
       const int64_t row = src_row[r];
       if (row >= 0)
@@ -263,7 +270,7 @@ read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const fl
             __ldcs(reinterpret_cast<const uint4*>(rope + row * rope_stride) + c);
     }
   } else {
-    for (int i = threadIdx.x; i < kReadRows * d_r; i += kReadThreads) {
+    for (int i = threadIdx.x; i < rows_per_block * d_r; i += kReadThreads) {
       const int r = i / d_r, c = i % d_r;
       const int64_t row = src_row[r];
       if (row >= 0) out[(r0 + r) * out_stride + d_c + c] = rope[row * rope_stride + c];

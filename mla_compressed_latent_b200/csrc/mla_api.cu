@@ -726,8 +726,10 @@ int latent_cache_args(const mla_dims_t* dims, int32_t dtype, const mla_latent_ca
 }  // namespace
 
 namespace {
-// How the 8-bit append projects: a wide tile (three 128-feature tiles per CTA) for token counts whose blocks
-// of 128 fill a good part of the SMs, K cut so that the rest is filled; else the split of a1.
+// How the 8-bit append projects. With many tokens the projection is bound by what L2 delivers (about 9.5
+// TB/s to all SMs, measured), so it takes the tile that moves the fewest bytes per product: 256 features x 256
+// tokens, all 512 accumulator columns, 64 KB a K chunk of 64 (4096 tokens, C = 7168: 64 us with tiles of 128 x
+// 128, 49 us with 384 x 128, XX us so). K is cut so that the tiles fill the SMs. Fewer tokens: the split of a1.
 struct AppendPlan {
   bool tc, wide;
   int ks;
@@ -737,7 +739,7 @@ AppendPlan append_fp8_plan(int32_t dtype, int n_tok, int C, int N) {
   AppendPlan a{append_on_tc(dtype, C, N), false, 0};
   a.wide = a.tc && n_tok >= kWideTokens;
   if (a.wide) {
-    const int ctas = ((N + 127) / 128 + 2) / 3 * ((n_tok + 127) / 128), chunks = C / mla::gemm::kBK;
+    const int ctas = ((N + 127) / 128 + 1) / 2 * ((n_tok + 255) / 256), chunks = C / mla::gemm::kBK;
     const int ks = std::max(1, std::min(num_sms() / ctas, chunks));
     const int per = (chunks + ks - 1) / ks;
     a.ks = (chunks + per - 1) / per;
@@ -792,7 +794,10 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
       p.part = part;
       p.w_early = 1;
       mla::gemm::Problem pr = with_sms({w_dkv_kr, x, 1, C, N, n_tok, ks});
-      if (plan.wide) pr.m_per_cta = 3;
+      if (plan.wide) {
+        pr.m_per_cta = 2;
+        pr.tokens = 256;
+      }
       if (int e = mla::gemm::run(pr, p, st)) return e;
     } else {
       const int k_chunk = ((C + ks - 1) / ks + 63) / 64 * 64;
@@ -802,7 +807,8 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
              (const T*)w_dkv_kr, N, k_chunk, part, (T*)nullptr);
     }
     if (rows_in_warps) {
-      mla::launch_pdl(mla::cache8::append_fp8_rows_kernel<T>, dim3((n_tok + mla::cache8::kRowWarps - 1) / mla::cache8::kRowWarps),
+      const int blocks = std::min((n_tok + mla::cache8::kRowWarps - 1) / mla::cache8::kRowWarps, 2 * num_sms());
+      mla::launch_pdl(mla::cache8::append_fp8_rows_kernel<T>, dim3(blocks),
                       dim3(32 * mla::cache8::kRowWarps), 0, st, (const float*)part, ks, n_tok, s_q, dims->d_c, dims->d_r,
                       (const T*)gamma, dims->rms_eps, dims->rope_base, seqlens, block_table, max_pages,
                       const_cast<uint8_t*>(cache->codes), cache->code_stride, const_cast<float*>(cache->scales),
@@ -831,7 +837,9 @@ int mla_read_latent_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, const 
   if (!stride_ok(out_stride, dtype, (int64_t)dims->d_c + dims->d_r)) return MLA_ERR_INVALID_ARG;
   if ((rc = fp8_cache_args(dims, dtype, cache))) return rc;
   if (dims->d_c % 16) return MLA_ERR_UNSUPPORTED;
-  const int64_t blocks = (n_rows + mla::cache8::kReadRows - 1) / mla::cache8::kReadRows;
+  // few rows: blocks of 8, so that they spread over the SMs
+  const int rows_per_block = n_rows <= (int64_t)mla::cache8::kReadRows * num_sms() ? 8 : mla::cache8::kReadRows;
+  const int64_t blocks = (n_rows + rows_per_block - 1) / rows_per_block;
   if (blocks > INT32_MAX) return MLA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto run = [&](auto zero) -> int {
@@ -839,7 +847,7 @@ int mla_read_latent_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, const 
     mla::launch_pdl(mla::cache8::read_fp8_kernel<T>, dim3((unsigned)blocks), dim3(mla::cache8::kReadThreads), 0, st,
                     (const uint8_t*)cache->codes, cache->code_stride, (const float*)cache->scales,
                     (const T*)cache->rope, cache->rope_stride, cache->num_pages, block_table, max_pages, first,
-                    row_offsets, B, n_rows, dims->d_c, dims->d_r, (T*)out, out_stride);
+                    row_offsets, B, n_rows, rows_per_block, dims->d_c, dims->d_r, (T*)out, out_stride);
     return launch_status();
   };
   return dtype == MLA_F32 ? run(0.f) : run(__nv_bfloat16());

@@ -5,15 +5,19 @@
 // for every token v, over the pages p it sees. The softmax runs over the pages of one head and the sum over
 // the heads of one page, so a token needs all of u before it can write anything. u never leaves the
 // SM: the 128 heads are the M rows of the product and pages its N columns, and an accumulator of 128
-// lanes x 512 columns is exactly the tensor memory of one SM. A cluster of 1, 2, 4 or 8 CTAs takes one
+// lanes x 512 columns is exactly the tensor memory of one SM. A cluster of 1 to 8 CTAs takes one
 // token, up to 512 pages each; the CTAs swap each head's running maximum and sum through
 // distributed shared memory, and read their u a second time to sum the masses over the heads.
 // Bound: q (128 rows) and the keys, read once per token (keys of one sequence come from L2 after the first
 // token); 2 · 128 · (d_c + d_r) operations a page.
 //
 // Warps 0-7 gather the keys (a page's key lies wherever the block table says, so rows are fetched 16 bytes a
-// thread with asynchronous copies into 128-byte swizzled tiles of 64 pages x 64 columns, six stages
-// ahead), then turn the accumulator into masses; warp 8 loads q by TMA and issues the products.
+// thread with asynchronous copies into 128-byte swizzled stages of 128 pages x 64 columns), then turn
+// the accumulator into masses; warp 8 loads q by TMA and issues the products. The column chunks are the
+// outer loop and the page tiles the inner one: all tiles' accumulators live at once, so only the chunk of q
+// at hand has to be in shared memory and ten stages (160 KB, eight of them in flight) are left for
+// the keys. What bounds a long context is how many key bytes are in flight: with q resident (64 KB of
+// stages) 8 sequences of 16K-128K positions took 33 us, XX us so.
 #pragma once
 
 #include "common.cuh"
@@ -26,20 +30,22 @@ namespace mla {
 namespace score {
 
 constexpr int kH = 128;               // accumulator rows: heads, padded
-constexpr int kTile = 64;             // pages per product
+constexpr int kTile = 128;            // pages per product
 constexpr int kMaxPages = 512;        // pages per CTA: the accumulator's columns
 constexpr int kMaxChunks = 9;         // 64-column chunks of a row of up to 576 values
-constexpr int kStages = 8;
-constexpr int kAhead = 6;             // stages a thread's copies run ahead of what it has handed over
+constexpr int kStages = 10;
+constexpr int kAhead = 8;             // stages a thread's copies run ahead of what it has handed over
 constexpr int kStageBytes = kTile * 128;
 constexpr int kQChunkBytes = kH * 128;
 constexpr int kWorkers = 256;         // threads of warps 0-7
 constexpr int kThreads = kWorkers + 32;
 constexpr int kMaxCluster = 8;
-constexpr int kOffRing = kMaxChunks * kQChunkBytes;
+constexpr int kQSlots = 3;            // chunks of q in shared memory
+constexpr int kMaxTiles = kMaxPages / kTile;
+constexpr int kOffRing = kQSlots * kQChunkBytes;
 constexpr int kOffStats = kOffRing + kStages * kStageBytes;            // float2 [cluster][2][kH]
 constexpr int kOffBar = kOffStats + kMaxCluster * 2 * kH * 8;
-enum Bar { FULL = 0, EMPTY = FULL + kStages, Q_FULL = EMPTY + kStages, DONE = Q_FULL + kMaxChunks, NUM_BARS };
+enum Bar { FULL = 0, EMPTY = FULL + kStages, Q_FULL = EMPTY + kStages, Q_EMPTY = Q_FULL + kQSlots, DONE = Q_EMPTY + kQSlots, NUM_BARS };
 constexpr int kOffSlot = kOffBar + NUM_BARS * 8;
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;   // + alignment slack of the dynamic base
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -80,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) { ptx::mbar_init(bar(FULL + i), kWorkers / 32); ptx::mbar_init(bar(EMPTY + i), 1); }
-    for (int i = 0; i < kMaxChunks; ++i) ptx::mbar_init(bar(Q_FULL + i), 1);
+    for (int i = 0; i < kQSlots; ++i) { ptx::mbar_init(bar(Q_FULL + i), 1); ptx::mbar_init(bar(Q_EMPTY + i), 1); }
     ptx::mbar_init(bar(DONE), 1);
     *abort = 0;
     ptx::fence_mbar_init();
@@ -101,41 +107,52 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
     if (tid == 0 && rank == 0) report(MLA_ERR_DEVICE_CHECK);
     n_all = p.max_pages;
   }
-  const int per = ((n_all + csize - 1) / csize + kTile - 1) / kTile * kTile;
+  const int per = ((n_all + csize - 1) / csize + 31) / 32 * 32;
   const int p0 = min(n_all, (int)rank * per), n = min(n_all - p0, per);
   const int tiles = (n + kTile - 1) / kTile, chunks = (p.W + 63) / 64, total = tiles * chunks;
   float2* stats = reinterpret_cast<float2*>(gbase + kOffStats);
 
   if (warp < 8) {
-    // ---- gather: rows r0 and r0 + 32 of each 64-page tile, one 16-byte piece of the chunk's 128 bytes
+    // ---- gather: rows r0 + 32 u of each tile, one 16-byte piece of the chunk's 128 bytes
+    constexpr int kU = kTile / 32;
     const int r0 = tid >> 3, piece = tid & 7;
     const uint32_t dst0 = base + kOffRing + (uint32_t)r0 * 128u + (((uint32_t)piece ^ ((uint32_t)r0 & 7u)) << 4);
     const int32_t* table = p.block_table + (int64_t)seq * p.max_pages + p0;
-    auto page_of = [&](int row) -> int { return row < n ? table[row] : -1; };
-    int next0 = page_of(r0), next1 = page_of(r0 + 32), pg0 = -1, pg1 = -1;
+    int pg[kMaxTiles][kU];   // the pages of this thread's rows, tile by tile; -1: zeros
+#pragma unroll
+    for (int t = 0; t < kMaxTiles; ++t)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int row = t * kTile + r0 + 32 * u;
+        pg[t][u] = row < n ? table[row] : -1;
+      }
+#pragma unroll
+    for (int t = 0; t < kMaxTiles; ++t)
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (pg[t][u] < 0 || pg[t][u] >= p.num_pages) {
+          if (t * kTile + r0 + 32 * u < n) report(MLA_ERR_DEVICE_CHECK);
+          pg[t][u] = -1;
+        }
     bool live = true;
     for (int i = 0, kc = 0, tile = 0; i < total + kAhead; ++i) {
       if (i < total && live) {
-        if (kc == 0) {   // a new tile: its page ids were read a tile ago
-          pg0 = next0;
-          pg1 = next1;
-          if (tile * kTile + r0 < n && (pg0 < 0 || pg0 >= p.num_pages)) { report(MLA_ERR_DEVICE_CHECK); pg0 = -1; }
-          if (tile * kTile + r0 + 32 < n && (pg1 < 0 || pg1 >= p.num_pages)) { report(MLA_ERR_DEVICE_CHECK); pg1 = -1; }
-          next0 = page_of((tile + 1) * kTile + r0);
-          next1 = page_of((tile + 1) * kTile + r0 + 32);
-        }
         const int s = i % kStages;
         if (i >= kStages) live = __all_sync(0xffffffffu, gemm::wait(bar(EMPTY + s), ((i / kStages) & 1u) ^ 1u, abort));
         if (live) {
           const int col = kc * 64 + piece * 8;
           const bool in = col < p.W;
           const uint32_t dst = dst0 + (uint32_t)s * kStageBytes;
-          const __nv_bfloat16* k0 = p.keys + (int64_t)max(pg0, 0) * p.key_stride + (in ? col : 0);
-          const __nv_bfloat16* k1 = p.keys + (int64_t)max(pg1, 0) * p.key_stride + (in ? col : 0);
-          cp_async16(dst, k0, in && pg0 >= 0);
-          cp_async16(dst + 32 * 128, k1, in && pg1 >= 0);
+          const __nv_bfloat16* k0 = p.keys + (in ? col : 0);
+#pragma unroll
+          for (int t = 0; t < kMaxTiles; ++t) {
+            if (t != tile) continue;
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+              cp_async16(dst + u * 32 * 128, k0 + (int64_t)max(pg[t][u], 0) * p.key_stride, in && pg[t][u] >= 0);
+          }
         }
-        if (++kc == chunks) { kc = 0; ++tile; }
+        if (++tile == tiles) { tile = 0; ++kc; }
       }
       cp_async_commit();
       if (i >= kAhead && live) {   // this warp's copies of stage i - kAhead have landed: hand it over
@@ -148,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
     cp_async_wait<0>();
     if (!live) *abort = 1;
     // ---- per head (= lane of the accumulator): maximum and sum of exponentials over this CTA's pages; warps
-    // 0-3 take the even tiles, 4-7 the odd ones
+    // 0-3 take the first half of each tile, 4-7 the second
     __syncwarp();
     const int q4 = warp & 3, half = warp >> 2, head = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
@@ -156,26 +173,34 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
     ptx::tc_fence_after();
     const float s2 = p.scale_log2;
     float m = -INFINITY, l = 0.f;
-    for (int t = half; t < tiles && ok; t += 2) {
+    for (int t = 0; t < tiles && ok; ++t) {
       const int valid = n - t * kTile;
-#pragma unroll 1
-      for (int c = 0; c < kTile; c += 32) {
-        uint32_t r[32];
-        ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c), r);
-        ptx::tmem_wait_ld_regs(r);
-        float mt = m;
+      const int c = half * (kTile / 2);
+      if (c >= valid) continue;
+      uint32_t r0v[32], r1v[32];
+      ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c), r0v);
+      ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c + 32), r1v);
+      ptx::tmem_wait_ld_regs(r0v);
+      ptx::tmem_wait_ld_regs(r1v);
+      if (valid < c + 64) {   // pages past the end
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c + j < valid) mt = fmaxf(mt, __uint_as_float(r[j]));
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c + j < valid) sum += ptx::ex2_approx((__uint_as_float(r[j]) - mt) * s2);
-        if (c < valid) {
-          l = l * ptx::ex2_approx((m - mt) * s2) + sum;
-          m = mt;
+        for (int j = 0; j < 32; ++j) {
+          if (c + j >= valid) r0v[j] = 0xff800000u;
+          if (c + 32 + j >= valid) r1v[j] = 0xff800000u;
         }
       }
+      float mx[4] = {m, m, m, m}, sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        mx[j & 3] = fmaxf(mx[j & 3], fmaxf(__uint_as_float(r0v[j]), __uint_as_float(r1v[j])));
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), off = -mt * s2;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        sm[j & 3] += ptx::ex2_approx(fmaf(__uint_as_float(r0v[j]), s2, off));
+        sm[(j + 2) & 3] += ptx::ex2_approx(fmaf(__uint_as_float(r1v[j]), s2, off));
+      }
+      l = l * ptx::ex2_approx((m - mt) * s2) + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
+      m = mt;
     }
     for (int r = 0; r < csize; ++r) {
       const uint32_t at = ptx::map_to_cta(base + kOffStats + (uint32_t)(((int)rank * 2 + half) * kH + head) * 8u, (uint32_t)r);
@@ -183,38 +208,52 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
       ptx::st_cluster_f32(at + 4u, l);
     }
   } else {
-    // ---- q by TMA, one barrier per 64-column chunk, then the products
-    if (lane == 0 && tiles > 0) {
-      for (int kc = 0; kc < chunks; ++kc) {
-        ptx::mbar_arrive_expect_tx(bar(Q_FULL + kc), kQChunkBytes);
-        ptx::tma_load_2d(base + kc * kQChunkBytes, &tm_q, kc * 64, v * p.H, bar(Q_FULL + kc));
-        ptx::tma_load_2d(base + kc * kQChunkBytes + kQChunkBytes / 2, &tm_q, kc * 64, v * p.H + 64, bar(Q_FULL + kc));
-      }
-    }
+    // ---- q by TMA, chunk by chunk, and the products
+    auto load_q = [&](int kc) {   // (lane 0; its slot is free)
+      const int s = kc % kQSlots;
+      const uint32_t dst = base + s * kQChunkBytes;
+      ptx::mbar_arrive_expect_tx(bar(Q_FULL + s), kQChunkBytes);
+      ptx::tma_load_2d(dst, &tm_q, kc * 64, v * p.H, bar(Q_FULL + s));
+      ptx::tma_load_2d(dst + kQChunkBytes / 2, &tm_q, kc * 64, v * p.H + 64, bar(Q_FULL + s));
+    };
+    int loaded = 0;
+    if (tiles > 0)
+      for (; loaded < min(chunks, kQSlots - 1); ++loaded)
+        if (lane == 0) load_q(loaded);
     __syncwarp();
     const uint64_t qd = ptx::smem_desc_sw128(base, 16, 1024), kd = ptx::smem_desc_sw128(base + kOffRing, 16, 1024);
     bool live = true;
     for (int i = 0, kc = 0, tile = 0; i < total && live; ++i) {
-      const int s = i % kStages;
-      if (tile == 0) live = __all_sync(0xffffffffu, gemm::wait(bar(Q_FULL + kc), 0, abort));
+      const int s = i % kStages, qs = kc % kQSlots;
+      if (tile == 0) {
+        if (loaded < chunks) {   // the next chunk into the slot whose products were issued a chunk ago
+          live = __all_sync(0xffffffffu, gemm::wait(bar(Q_EMPTY + loaded % kQSlots), ((loaded / kQSlots) & 1u) ^ 1u, abort));
+          if (!live) break;
+          if (lane == 0) load_q(loaded);
+          ++loaded;
+          __syncwarp();
+        }
+        live = __all_sync(0xffffffffu, gemm::wait(bar(Q_FULL + qs), (kc / kQSlots) & 1u, abort));
+      }
       live = live && __all_sync(0xffffffffu, gemm::wait(bar(FULL + s), (i / kStages) & 1u, abort));
       if (live && ptx::elect_one()) {
         ptx::tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          ptx::mma_ss(tmem + (uint32_t)(tile * kTile), qd + (uint64_t)(kc * (kQChunkBytes >> 4) + 2 * k),
+          ptx::mma_ss(tmem + (uint32_t)(tile * kTile), qd + (uint64_t)(qs * (kQChunkBytes >> 4) + 2 * k),
                       kd + (uint64_t)(s * (kStageBytes >> 4) + 2 * k), kIdesc, (kc | k) ? 1u : 0u);
         ptx::mma_commit(bar(EMPTY + s));
+        if (tile == tiles - 1) ptx::mma_commit(bar(Q_EMPTY + qs));
         if (i == total - 1) ptx::mma_commit(bar(DONE));
       }
       __syncwarp();
-      if (++kc == chunks) { kc = 0; ++tile; }
+      if (++tile == tiles) { tile = 0; ++kc; }
     }
     if (total == 0 && lane == 0) ptx::mbar_arrive(bar(DONE));
     if (!live) {
       *abort = 1;
       if (ptx::elect_one()) ptx::mma_commit(bar(DONE));   // what was issued completes before the exit
-      for (int kc = 0; kc < chunks; ++kc) gemm::wait(bar(Q_FULL + kc), 0);   // and so do the loads
+      for (int kc = max(0, loaded - kQSlots); kc < loaded; ++kc) gemm::wait(bar(Q_FULL + kc % kQSlots), (kc / kQSlots) & 1u);   // and so do the loads
       gemm::wait(bar(DONE), 0);
     }
     __syncwarp();
@@ -232,34 +271,35 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
       const float2 st = stats[r * kH + head];
       if (st.y != 0.f) l += st.y * ptx::ex2_approx((st.x - m) * s2);
     }
-    const float inv = head < p.H ? 1.f / l : 0.f;
+    const float inv = head < p.H ? 1.f / l : 0.f, off = -m * s2;
     // masses e^(u - m) / l, summed over the warp's 32 heads: at each step a lane keeps half of its columns and
-    // adds the other lane's values of them, so that lane j ends with column j
+    // adds the other lane's values of them, so that of 64 columns lane j ends with 2 j and 2 j + 1
     float* colsum = reinterpret_cast<float*>(gbase);   // [4][kMaxPages], over the query (its products are done)
-    for (int t = half; t < tiles; t += 2) {
-#pragma unroll 1
-      for (int c = 0; c < kTile; c += 32) {
-        if (t * kTile + c >= n) break;
-        uint32_t r[32];
-        ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c), r);
-        ptx::tmem_wait_ld_regs(r);
-        float a[32];
+    for (int t = 0; t < tiles; ++t) {
+      const int c = half * (kTile / 2);
+      if (t * kTile + c >= n) break;
+      uint32_t r0v[32], r1v[32];
+      ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c), r0v);
+      ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c + 32), r1v);
+      ptx::tmem_wait_ld_regs(r0v);
+      ptx::tmem_wait_ld_regs(r1v);
+      float a[64];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float e = ptx::ex2_approx((__uint_as_float(r[j]) - m) * s2) * inv;
-          a[j] = head < p.H ? e : 0.f;   // (rows past the last head may hold anything)
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const bool up = (lane & o) != 0;
-#pragma unroll
-          for (int j = 0; j < o; ++j) {
-            const float send = up ? a[j] : a[j + o], keep = up ? a[j + o] : a[j];
-            a[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
-        }
-        colsum[q4 * kMaxPages + t * kTile + c + lane] = a[0];
+      for (int j = 0; j < 64; ++j) {
+        const float e = ptx::ex2_approx(fmaf(__uint_as_float(j < 32 ? r0v[j & 31] : r1v[j & 31]), s2, off)) * inv;
+        a[j] = head < p.H ? e : 0.f;   // (rows past the last head may hold anything)
       }
+#pragma unroll
+      for (int o = 32; o > 1; o >>= 1) {
+        const bool up = (lane & (o >> 1)) != 0;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+          const float send = up ? a[j] : a[j + o], keep = up ? a[j + o] : a[j];
+          a[j] = keep + __shfl_xor_sync(0xffffffffu, send, o >> 1);
+        }
+      }
+      // lane j holds columns 2 j and 2 j + 1
+      *reinterpret_cast<float2*>(&colsum[q4 * kMaxPages + t * kTile + c + 2 * lane]) = make_float2(a[0], a[1]);
     }
     ptx::tc_fence_before();
     ptx::named_bar_sync(1, kWorkers);
@@ -281,6 +321,33 @@ inline bool supported(const mla_dims_t* d, int32_t dtype, int64_t rows, int32_t 
          rows * d->H <= INT32_MAX && rows * kMaxCluster <= INT32_MAX;
 }
 
+// Clusters of c CTAs that the device runs at once, asked once.
+inline int resident_clusters(int c, int num_sms) {
+  static int cached[64][kMaxCluster + 1] = {{0}};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool known = dev >= 0 && dev < 64;
+  if (known && cached[dev][c]) return cached[dev][c];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(num_sms / c * c));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, score_kernel, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = num_sms / c;
+  }
+  if (known) cached[dev][c] = n;
+  return n;
+}
+
 inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const void* q_abs, const void* keys, int64_t key_stride,
                         int32_t num_pages, const int32_t* block_table, int32_t max_pages, const int32_t* seqlens,
                         float scale, float* scores, int num_sms, cudaStream_t st) {
@@ -295,11 +362,11 @@ inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const vo
   const int W = d->d_c + d->d_r;
   CUtensorMap tm_q;   // q_abs as [rows * H, W]: boxes of 64 heads x 64 columns
   if (!tmap::make_bf16_sw128(&tm_q, q_abs, W, (int64_t)rows * d->H, W, 64)) return MLA_ERR_INVALID_ARG;
-  // as few CTAs a token as hold its pages, doubled while the tokens leave SMs idle and a CTA would still
-  // have a whole tile
-  int c = 1;
-  while (c < kMaxCluster && c * kMaxPages < max_pages) c *= 2;
-  while (c < kMaxCluster && (int64_t)rows * 2 * c <= num_sms && max_pages > c * kTile) c *= 2;
+  // as few CTAs a token as hold its pages, more while all tokens' clusters still run at once and a CTA has
+  // half a tile
+  int c = (max_pages + kMaxPages - 1) / kMaxPages;
+  // (a cluster lies within one GPC: fewer than num_sms / c of them may run at once)
+  while (c < kMaxCluster && rows <= resident_clusters(c + 1, num_sms) && max_pages > c * kTile / 2) ++c;
   Params prm{reinterpret_cast<const __nv_bfloat16*>(keys), key_stride, block_table, max_pages, num_pages, seqlens, s_q,
              d->H, W, scale * 1.4426950408889634f, scores};
   cudaLaunchConfig_t cfg = {};
