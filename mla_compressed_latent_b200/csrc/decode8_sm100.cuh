@@ -200,7 +200,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
     const int32_t* list = p.page_list + (long long)v * p.k;
     const int seq = v / p.s_q, pg = list[t], before = t > 0 ? list[t - 1] : -1, vis = visible(v);
     int page = -1;
-    if (pg > before && pg < p.max_pages && vis > 0 && pg <= (vis - 1) / kTile)
+    if (pg >= 0 && pg > before && pg < p.max_pages && vis > 0 && pg <= (vis - 1) / kTile)
       page = p.block_table[(long long)seq * p.max_pages + pg];
     if (page < 0 || page >= p.num_pages) {
       if (may_report) report(MLA_ERR_DEVICE_CHECK);

@@ -528,17 +528,50 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       return p.seqlens[bb] - (p.s_q - 1 - tok);
     }
   };
-  // pool page of the item's tile t; -1 when the list names no visible page there or is not ascending
-  auto page_at = [&](int bb, int t) -> int {
-    if constexpr (kSparse) {
-      const int32_t* list = p.page_list + (long long)bb * p.list_k;
-      const int seq = bb / p.list_s_q, pg = list[t], before = t > 0 ? list[t - 1] : -1;
-      const int vis = p.seqlens[seq] - (p.list_s_q - 1 - bb % p.list_s_q);
-      if (pg <= before || pg >= p.max_pages || pg > (vis - 1) / kTile || vis <= 0) return -1;
-      return p.block_table[(long long)seq * p.max_pages + pg];
-    } else {
-      return p.block_table[(long long)bb * p.max_pages + t];
+  // Pool pages of a segment's tiles, in order. Dense: the block table. Sparse: the table at the listed page, -1
+  // when the list names no visible page there or is not ascending; the list is read two tiles ahead
+  // and the table one, so that the two dependent loads wait for nothing (with both in the tile's own
+  // turn the ring stood idle for their latency).
+  struct PageWalk {
+    const int32_t* table;
+    const int32_t* list;
+    int n, max_pages, pages_seen, i, before, entry, page;
+    __device__ int lookup(int e) const { return e >= 0 && e > before && e < max_pages && e < pages_seen ? table[e] : -1; }
+    __device__ int next() {
+      if constexpr (kSparse) {
+        const int now = page;
+        before = entry_before;
+        page = i + 1 < n ? lookup(entry) : -1;
+        entry_before = entry;
+        if (i + 2 < n) entry = list[i + 2];
+        ++i;
+        return now;
+      } else {
+        return table[i++];
+      }
     }
+    int entry_before;
+  };
+  auto walk = [&](int bb, int lo, int hi) -> PageWalk {
+    PageWalk w{};
+    w.i = lo;
+    w.n = hi;
+    w.max_pages = p.max_pages;
+    if constexpr (kSparse) {
+      const int seq = bb / p.list_s_q;
+      const int vis = p.seqlens[seq] - (p.list_s_q - 1 - bb % p.list_s_q);
+      w.table = p.block_table + (long long)seq * p.max_pages;
+      w.list = p.page_list + (long long)bb * p.list_k;
+      w.pages_seen = vis > 0 ? (vis + kTile - 1) / kTile : 0;
+      w.before = lo > 0 ? w.list[lo - 1] : -1;
+      const int first = w.list[lo];
+      w.page = w.lookup(first);
+      w.entry_before = first;
+      w.entry = lo + 1 < hi ? w.list[lo + 1] : 0;
+    } else {
+      w.table = p.block_table + (long long)bb * p.max_pages;
+    }
+    return w;
   };
 
   if (rank == 0) {
@@ -549,6 +582,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
         bool ok = true;
         uint32_t gi = 0;
         while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+          PageWalk pages = walk(b, t_lo, t_hi);
           // the sequence's absorbed query first: box (column block cb, head half rh)
           for (int qg = 0; qg < kQGroups && ok; ++qg, ++gi) {
             const uint32_t s = gi % kRing;
@@ -560,7 +594,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
             }
           }
           for (int t = t_lo; t < t_hi && ok; ++t, ++it) {
-            int page = page_at(b, t);   // issued before the wait
+            int page = pages.next();   // issued before the wait
             for (int q = 0; q < kGroupsPerTile && ok; ++q, ++gi) {
               const uint32_t s = gi % kRing;
               if (!(ok = wait_bar(bar(K_EMPTY + s), ((gi / kRing) & 1u) ^ 1u, abort_addr, false))) break;
@@ -828,9 +862,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
         uint32_t it = 0;
         bool ok = true;
         while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+          PageWalk pages = walk(b, t_lo, t_hi);
           for (int t = t_lo; t < t_hi && ok; ++t, ++it) {
             const uint32_t s = it % kVStages;
-            int page = page_at(b, t);   // issued before the wait
+            int page = pages.next();   // issued before the wait
             if (!(ok = wait_bar(bar(V_EMPTY + s), ((it / kVStages) & 1u) ^ 1u, abort_addr, false))) break;
             if (page < 0 || page >= p.num_pages) page = p.num_pages;   // reported by the score CTA
             const uint32_t dst = base + kOffV + s * kVStageBytes;

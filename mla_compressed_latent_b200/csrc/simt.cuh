@@ -574,7 +574,7 @@ decode_simt_kernel(DecodeArgs A) {
       int64_t row = -1;
       if (p < hi && list) {
         const int i = p >> 6, pg = list[i], before = i > 0 ? list[i - 1] : -1;
-        if (pg <= before || pg >= A.max_pages || (int64_t)pg * 64 >= vis) {
+        if (pg < 0 || pg <= before || pg >= A.max_pages || (int64_t)pg * 64 >= vis) {
           report(MLA_ERR_DEVICE_CHECK);
         } else {
           p = pg * 64 + (p & 63);

@@ -7,6 +7,7 @@ the computation runs in the library's CUDA kernels; a failing call raises MlaErr
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -280,6 +281,8 @@ def mla_decode_absorbed_fp8(dims: Dims, q_abs, cache: LatentCacheFp8, block_tabl
 # These calls check what they are given: a tensor of another shape or dtype, one that is not contiguous
 # where the library wants rows laid end to end, or one that is not on the current device raises before
 # anything is enqueued.
+# The checks of one tensor are a single condition (a decode step's calls are short, and so is the time to issue
+# them); what was wrong is found out when it fails.
 def _current(t: torch.Tensor) -> int:
     """The current device, which has to hold t (the library enqueues on it)."""
     if not t.is_cuda:
@@ -290,26 +293,26 @@ def _current(t: torch.Tensor) -> int:
     return dev
 
 
-def _need(dev: int, name: str, t: torch.Tensor, shape, dtype) -> int:
-    """data_ptr of a contiguous tensor of this shape and dtype on device `dev`."""
+def _refuse(dev: int, name: str, t: torch.Tensor, dtype, what: str):
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{name}: libmla takes tensors of the current device (cuda:{dev}), got {t.device}")
+    raise ValueError(f"{name}: expected {what}, got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _need(dev: int, name: str, t: torch.Tensor, shape, dtype) -> int:
+    """data_ptr of a contiguous tensor of this shape and dtype on device `dev`."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(dev, name, t, dtype, f"a contiguous tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
 def _need_rows(dev: int, name: str, t: torch.Tensor, rows: int, width: int, dtype) -> None:
     """A matrix of at least `rows` rows of `width` values laid end to end (rows may be strided)."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected at least {rows} rows of {width} values, got {tuple(t.shape)} "
-                         f"with strides {t.stride()}")
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name}: libmla takes tensors of the current device (cuda:{dev}), got {t.device}")
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or \
+            (width > 1 and t.stride(1) != 1):
+        _refuse(dev, name, t, dtype, f"at least {rows} rows of {width} values")
 
 
 def _cache_arg(dev: int, dims: Dims, cache, dtype):
@@ -335,12 +338,21 @@ def _table(dev: int, B: int, block_table, seqlens):
             None if seqlens is None else _need(dev, "seqlens", seqlens, (B,), torch.int32))
 
 
-def _space(dev: int, nbytes: int, workspace):
+def _new(dev: int, stream, make, *shape, dtype):
+    """A tensor made by `make` (torch.empty, torch.zeros) for use on `stream`: taken from that stream's pool,
+    so that no memory another stream still works on is handed out, nor this one's while it does."""
+    if stream is None:
+        return make(*shape, dtype=dtype, device=torch.device("cuda", dev))
+    with torch.cuda.stream(stream):
+        return make(*shape, dtype=dtype, device=torch.device("cuda", dev))
+
+
+def _space(dev: int, nbytes: int, workspace, stream):
     """(workspace or None, its pointer, its size): taken from torch's allocator when none is given."""
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+        workspace = _new(dev, stream, torch.empty, nbytes, dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -348,10 +360,21 @@ def _space(dev: int, nbytes: int, workspace):
 
 def _stream_on(dev: int, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev)
     if stream.device_index != dev:
         raise ValueError(f"stream: expected a stream of the current device (cuda:{dev})")
     return stream.cuda_stream
+
+
+# the current stream's handle, without making a Stream object where this torch has the short way
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(fn: str, dev: int, dims: Dims, *args) -> int:
+    """A workspace size of the library (they depend on shapes and on the device alone)."""
+    return getattr(L.load(), fn)(ctypes.byref(dims.c()), *args)
 
 
 def _width(dims: Dims) -> int:
@@ -373,8 +396,7 @@ def mla_append_cache_fp8(dims: Dims, x, w_dkv_kr, gamma, seqlens, block_table, c
     table, max_pages, lens = _table(dev, B, block_table, seqlens)
     cc = _cache_arg(dev, dims, cache, x.dtype)
     d = dims.c()
-    need = lib.mla_append_fp8_workspace_size(ctypes.byref(d), dt, B, s_q, C)
-    workspace, ws, wsb = _space(dev, need, workspace)
+    workspace, ws, wsb = _space(dev, _bytes("mla_append_fp8_workspace_size", dev, dims, dt, B, s_q, C), workspace, stream)
     rc = lib.mla_append_cache_fp8(ctypes.byref(d), dt, B, s_q, px, C, pw, pg, lens, table, max_pages, ctypes.byref(cc),
                                   ws, wsb, _stream_on(dev, stream))
     _check("mla_append_cache_fp8", rc)
@@ -430,11 +452,11 @@ def mla_score_pages(dims: Dims, q_abs, keys, block_table, seqlens, scores=None, 
     table, max_pages, lens = _table(dev, B, block_table, seqlens)
     _need_rows(dev, "keys", keys, 1, _width(dims), q_abs.dtype)
     if scores is None:
-        scores = torch.zeros(B, s_q, max_pages, dtype=torch.float32, device=q_abs.device)
+        scores = _new(dev, stream, torch.zeros, B, s_q, max_pages, dtype=torch.float32)
     ps = _need(dev, "scores", scores, (B, s_q, max_pages), torch.float32)
     d = dims.c()
-    need = lib.mla_score_pages_workspace_size(ctypes.byref(d), dt, B, s_q, max_pages)
-    workspace, ws, wsb = _space(dev, need, workspace)
+    need = _bytes("mla_score_pages_workspace_size", dev, dims, dt, B, s_q, max_pages)
+    workspace, ws, wsb = _space(dev, need, workspace, stream)
     rc = lib.mla_score_pages(ctypes.byref(d), dt, B, s_q, pq, keys.data_ptr(), keys.stride(0), keys.shape[0], table,
                              max_pages, lens, ps, ws, wsb, _stream_on(dev, stream))
     _check("mla_score_pages", rc)
@@ -453,9 +475,9 @@ def mla_select_pages(dims: Dims, scores, seqlens, k: int, n_first: int = 0, n_re
     ps = _need(dev, "scores", scores, (B, s_q, max_pages), torch.float32)
     lens = _need(dev, "seqlens", seqlens, (B,), torch.int32)
     if pages is None:
-        pages = torch.empty(B, s_q, k, dtype=torch.int32, device=scores.device)
+        pages = _new(dev, stream, torch.empty, B, s_q, k, dtype=torch.int32)
     if counts is None:
-        counts = torch.empty(B, s_q, dtype=torch.int32, device=scores.device)
+        counts = _new(dev, stream, torch.empty, B, s_q, dtype=torch.int32)
     pp = _need(dev, "pages", pages, (B, s_q, k), torch.int32)
     pc = _need(dev, "counts", counts, (B, s_q), torch.int32)
     d = dims.c()
@@ -481,16 +503,16 @@ def mla_decode_absorbed_sparse(dims: Dims, q_abs, cache, block_table, seqlens, p
     pc = _need(dev, "counts", counts, (B, s_q), torch.int32)
     cc = _cache_arg(dev, dims, cache, q_abs.dtype)
     if o_lat is None:
-        o_lat = torch.empty(B, s_q, dims.H, dims.d_c, dtype=q_abs.dtype, device=q_abs.device)
+        o_lat = _new(dev, stream, torch.empty, B, s_q, dims.H, dims.d_c, dtype=q_abs.dtype)
     if lse is None:
-        lse = torch.empty(B, s_q, dims.H, dtype=torch.float32, device=q_abs.device)
+        lse = _new(dev, stream, torch.empty, B, s_q, dims.H, dtype=torch.float32)
     po = _need(dev, "o_lat", o_lat, (B, s_q, dims.H, dims.d_c), q_abs.dtype)
     pl = _need(dev, "lse", lse, (B, s_q, dims.H), torch.float32)
     fp8 = isinstance(cache, LatentCacheFp8)
     name = "mla_decode_absorbed_sparse_fp8" if fp8 else "mla_decode_absorbed_sparse"
-    size = lib.mla_decode_sparse_fp8_workspace_size if fp8 else lib.mla_decode_sparse_workspace_size
+    size = "mla_decode_sparse_fp8_workspace_size" if fp8 else "mla_decode_sparse_workspace_size"
     d = dims.c()
-    workspace, ws, wsb = _space(dev, size(ctypes.byref(d), dt, B, s_q, k), workspace)
+    workspace, ws, wsb = _space(dev, _bytes(size, dev, dims, dt, B, s_q, k), workspace, stream)
     rc = getattr(lib, name)(ctypes.byref(d), dt, B, s_q, pq, ctypes.byref(cc), table, max_pages, lens, pp, pc, k, po, pl,
                             ws, wsb, _stream_on(dev, stream))
     _check(name, rc)

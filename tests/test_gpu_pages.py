@@ -492,7 +492,7 @@ def test_sparse_decode_of_every_page_is_the_dense_decode():
 
 @pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("name", ["dsv3_b64_l4096", "smallem_fp32"])
-@pytest.mark.parametrize("bad", ["past the visible pages", "twice", "descending", "negative", "count", "pool"])
+@pytest.mark.parametrize("bad", ["past the visible pages", "twice", "descending", "negative", "two negative", "count", "pool"])
 def test_sparse_decode_reports_a_bad_list(name, bits, bad):
     """A bad entry is reported and not read; the other tokens' results stand."""
     lens = [64 * 6, 64 * 8 + 3]
@@ -510,6 +510,8 @@ def test_sparse_decode_reports_a_bad_list(name, bits, bad):
         sent[0, 0] = [2, 0, 5]
     elif bad == "negative":
         sent[0, 0, 0] = -4
+    elif bad == "two negative":   # ascending, but no page at all
+        sent[0, 0] = [-4, -3, 5]
     elif bad == "count":
         n[0] = 4
     else:
