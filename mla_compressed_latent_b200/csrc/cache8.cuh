@@ -85,11 +85,12 @@ __global__ void append_fp8_finish_kernel(const float* __restrict__ part, int ksp
 // no block waits between the sums, the norm, the scale and the stores; the rotation's frequencies are made
 // once per block. d_c % 16 == 0, (d_c + d_r) % 4 == 0, d_c <= 128 * kRowChunks, d_r <= 64 * kRowPairs, 16-byte
 // aligned slices. For 4096 tokens of 512 + 64 values in one slice: 104 us for a block a token, 9 us so.
-constexpr int kRowChunks = 8;     // float4 pieces of the latent row a lane may hold
+constexpr int kRowChunks = 8;     // most float4 pieces of the latent row a lane holds
 constexpr int kRowPairs = 4;      // rotated pairs a lane may hold
 constexpr int kRowWarps = 8;
 
-template <typename T>
+// kChunks: float4 pieces a lane holds (4: rows of up to 512 values).
+template <typename T, int kChunks>
 __global__ void __launch_bounds__(32 * kRowWarps)
 append_fp8_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, int s_q, int d_c, int d_r,
                        const T* __restrict__ gamma, float eps, float rope_base, const int32_t* __restrict__ seqlens,
@@ -115,36 +116,37 @@ append_fp8_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, in
     }
     if (row < 0) continue;
     const float* src = part + (int64_t)tok * N;
-    float4 z[kRowChunks];
+    float4 z[kChunks];
     float2 zr[kRowPairs];
 #pragma unroll
-    for (int j = 0; j < kRowChunks; ++j) z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < kChunks; ++j) z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kRowPairs; ++j) zr[j] = make_float2(0.f, 0.f);
-    for (int s = 0; s < ksplit; ++s) {   // a slice's loads all in flight
+#pragma unroll 3
+    for (int s = 0; s < ksplit; ++s) {   // three slices' loads in flight
       const float* sl = src + s * step;
-      float4 v[kRowChunks];
+      float4 v[kChunks];
       float2 r[kRowPairs];
 #pragma unroll
-      for (int j = 0; j < kRowChunks; ++j)
+      for (int j = 0; j < kChunks; ++j)
         v[j] = lane + 32 * j < chunks ? __ldcg(reinterpret_cast<const float4*>(sl) + lane + 32 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < kRowPairs; ++j)
         r[j] = lane + 32 * j < d_r / 2 ? __ldcg(reinterpret_cast<const float2*>(sl + d_c) + lane + 32 * j) : make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < kRowChunks; ++j) { z[j].x += v[j].x; z[j].y += v[j].y; z[j].z += v[j].z; z[j].w += v[j].w; }
+      for (int j = 0; j < kChunks; ++j) { z[j].x += v[j].x; z[j].y += v[j].y; z[j].z += v[j].z; z[j].w += v[j].w; }
 #pragma unroll
       for (int j = 0; j < kRowPairs; ++j) { zr[j].x += r[j].x; zr[j].y += r[j].y; }
     }
     float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < kRowChunks; ++j)
+    for (int j = 0; j < kChunks; ++j)
       ss += fmaf(z[j].x, z[j].x, z[j].y * z[j].y) + fmaf(z[j].z, z[j].z, z[j].w * z[j].w);
     ss = warp_sum(ss);
     const float inv = 1.0f / sqrtf(ss / (float)d_c + eps);
     float amax = 0.f;
 #pragma unroll
-    for (int j = 0; j < kRowChunks; ++j) {
+    for (int j = 0; j < kChunks; ++j) {
       const int c = lane + 32 * j;
       if (c < chunks) {
         z[j].x *= inv; z[j].y *= inv; z[j].z *= inv; z[j].w *= inv;
@@ -160,7 +162,7 @@ append_fp8_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, in
     const float safe = s > 0.f ? s : 1.f;
     uint8_t* dst = codes + row * code_stride;
 #pragma unroll
-    for (int j = 0; j < kRowChunks; ++j) {
+    for (int j = 0; j < kChunks; ++j) {
       const int c = lane + 32 * j;
       if (c < chunks) {
         const float v[4] = {z[j].x, z[j].y, z[j].z, z[j].w};
@@ -189,7 +191,7 @@ append_fp8_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, in
 // 32-way search of row_offsets, a thread per row walks on from there and looks its cache row up, and
 // then all threads move 16 codes each at a time.
 // =============================================================================================
-constexpr int kReadRows = 64;
+constexpr int kReadRows = 32;
 constexpr int kReadThreads = 256;
 
 template <typename T>
@@ -243,7 +245,7 @@ read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const fl
     const int r = i / pieces, c = i % pieces;
     const int64_t row = src_row[r];
     if (row < 0) continue;
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(codes + row * code_stride) + c);
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(codes + row * code_stride) + c);
     const float sc = src_scale[r];
     const uint32_t q[4] = {v.x, v.y, v.z, v.w};
     float f[16];

@@ -807,8 +807,10 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
              (const T*)w_dkv_kr, N, k_chunk, part, (T*)nullptr);
     }
     if (rows_in_warps) {
-      const int blocks = std::min((n_tok + mla::cache8::kRowWarps - 1) / mla::cache8::kRowWarps, 2 * num_sms());
-      mla::launch_pdl(mla::cache8::append_fp8_rows_kernel<T>, dim3(blocks),
+      const int blocks = std::min((n_tok + mla::cache8::kRowWarps - 1) / mla::cache8::kRowWarps, 4 * num_sms());
+      mla::launch_pdl(dims->d_c <= 512 ? mla::cache8::append_fp8_rows_kernel<T, 4>
+                                       : mla::cache8::append_fp8_rows_kernel<T, mla::cache8::kRowChunks>,
+                      dim3(blocks),
                       dim3(32 * mla::cache8::kRowWarps), 0, st, (const float*)part, ks, n_tok, s_q, dims->d_c, dims->d_r,
                       (const T*)gamma, dims->rms_eps, dims->rope_base, seqlens, block_table, max_pages,
                       const_cast<uint8_t*>(cache->codes), cache->code_stride, const_cast<float*>(cache->scales),

@@ -342,9 +342,9 @@ def _new(dev: int, stream, make, *shape, dtype):
     """A tensor made by `make` (torch.empty, torch.zeros) for use on `stream`: taken from that stream's pool,
     so that no memory another stream still works on is handed out, nor this one's while it does."""
     if stream is None:
-        return make(*shape, dtype=dtype, device=torch.device("cuda", dev))
+        return make(*shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return make(*shape, dtype=dtype, device=torch.device("cuda", dev))
+        return make(*shape, dtype=dtype, device=dev)
 
 
 def _space(dev: int, nbytes: int, workspace, stream):
@@ -372,9 +372,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 
 @functools.lru_cache(maxsize=1024)
+def _bytes_of(fn: str, dev: int, H: int, D: int, d_r: int, d_c: int, *args) -> int:
+    return getattr(L.load(), fn)(ctypes.byref(Dims(H, D, d_r, d_c, d_c).c()), *args)
+
+
 def _bytes(fn: str, dev: int, dims: Dims, *args) -> int:
-    """A workspace size of the library (they depend on shapes and on the device alone)."""
-    return getattr(L.load(), fn)(ctypes.byref(dims.c()), *args)
+    """A workspace size of the library: it depends on the head layout, the sizes and the device alone."""
+    return _bytes_of(fn, dev, dims.H, dims.D, dims.d_r, dims.d_c, *args)
 
 
 def _width(dims: Dims) -> int:
