@@ -1,4 +1,8 @@
 // The 8-bit latent cache written straight from the projection, and read back into the storage type.
+//
+// (These kernels start while the kernel before them may still be writing their inputs, and wait for it. Their
+// pointers carry no restrict qualifier, so that no input is read through the non-coherent path, whose loads
+// nothing orders behind that wait.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -40,9 +44,9 @@ __device__ __forceinline__ uint32_t e4m3x4_codes(const float* v, float safe) {
 // new token; d_c % 16 == 0.
 // =============================================================================================
 template <typename T>
-__global__ void append_fp8_finish_kernel(const float* __restrict__ part, int ksplit, int n_tok, int s_q, int d_c, int d_r,
-                                         const T* __restrict__ gamma, float eps, float rope_base,
-                                         const int32_t* __restrict__ seqlens, const int32_t* __restrict__ block_table,
+__global__ void append_fp8_finish_kernel(const float* part, int ksplit, int n_tok, int s_q, int d_c, int d_r,
+                                         const T* gamma, float eps, float rope_base,
+                                         const int32_t* seqlens, const int32_t* block_table,
                                          int max_pages, uint8_t* codes, int64_t code_stride, float* scales, T* rope,
                                          int64_t rope_stride, int num_pages, int groups) {
   extern __shared__ float z[];
@@ -92,9 +96,9 @@ constexpr int kRowWarps = 8;
 // kChunks: float4 pieces a lane holds (4: rows of up to 512 values).
 template <typename T, int kChunks>
 __global__ void __launch_bounds__(32 * kRowWarps)
-append_fp8_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, int s_q, int d_c, int d_r,
-                       const T* __restrict__ gamma, float eps, float rope_base, const int32_t* __restrict__ seqlens,
-                       const int32_t* __restrict__ block_table, int max_pages, uint8_t* codes, int64_t code_stride,
+append_fp8_rows_kernel(const float* part, int ksplit, int n_tok, int s_q, int d_c, int d_r,
+                       const T* gamma, float eps, float rope_base, const int32_t* seqlens,
+                       const int32_t* block_table, int max_pages, uint8_t* codes, int64_t code_stride,
                        float* scales, T* rope, int64_t rope_stride, int num_pages) {
   __shared__ double inv_freq[32 * kRowPairs];
   for (int i = threadIdx.x; i < d_r / 2; i += blockDim.x) inv_freq[i] = rope_inv_freq(i, d_r, rope_base);
@@ -196,10 +200,10 @@ constexpr int kReadThreads = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads)
-read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const float* __restrict__ scales,
-                const T* __restrict__ rope, int64_t rope_stride, int num_pages, const int32_t* __restrict__ block_table,
-                int max_pages, const int32_t* __restrict__ first, const int32_t* __restrict__ row_offsets, int B,
-                int64_t n_rows, int rows_per_block, int d_c, int d_r, T* __restrict__ out, int64_t out_stride) {
+read_fp8_kernel(const uint8_t* codes, int64_t code_stride, const float* scales,
+                const T* rope, int64_t rope_stride, int num_pages, const int32_t* block_table,
+                int max_pages, const int32_t* first, const int32_t* row_offsets, int B,
+                int64_t n_rows, int rows_per_block, int d_c, int d_r, T* out, int64_t out_stride) {
   __shared__ int64_t src_row[kReadRows];   // -1: nothing to write there
   __shared__ float src_scale[kReadRows];
   __shared__ int s_b;
@@ -213,7 +217,7 @@ read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const fl
     while (lo < hi) {
       const int step = (hi - lo + 31) / 32;
       const int at = lo + (lane + 1) * step;
-      const bool le = at <= hi && (int64_t)__ldg(row_offsets + at) <= r0;
+      const bool le = at <= hi && (int64_t)row_offsets[at] <= r0;
       const int n = __popc(__ballot_sync(0xffffffffu, le));   // offsets do not fall: the first n hold
       lo += n * step;
       hi = min(hi, lo + step - 1);
@@ -232,20 +236,21 @@ read_fp8_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const fl
       if (b + stride <= B && (int64_t)row_offsets[b + stride] <= r) b += stride;
     if (r < n_rows && b < B) {
       const int64_t p = (int64_t)(first ? first[b] : 0) + (r - row_offsets[b]);
-      if (r < row_offsets[b] || p < 0 || (p >> 6) >= max_pages) report(MLA_ERR_DEVICE_CHECK);
-      else row = cache_row(block_table + (int64_t)b * max_pages, (int)p, num_pages);
+      int page = -1;
+      if (r >= row_offsets[b] && p >= 0 && (p >> 6) < max_pages) page = block_table[(int64_t)b * max_pages + (p >> 6)];
+      if (page >= 0 && page < num_pages) row = (int64_t)page * 64 + (p & 63);
+      else report(MLA_ERR_DEVICE_CHECK);
     }
     src_row[threadIdx.x] = row;
     src_scale[threadIdx.x] = row >= 0 ? scales[row] : 0.f;
   }
   __syncthreads();
   const int pieces = d_c / 16;
-#pragma unroll 4
   for (int i = threadIdx.x; i < rows_per_block * pieces; i += kReadThreads) {
     const int r = i / pieces, c = i % pieces;
     const int64_t row = src_row[r];
     if (row < 0) continue;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(codes + row * code_stride) + c);
+    const uint4 v = *(reinterpret_cast<const uint4*>(codes + row * code_stride) + c);
     const float sc = src_scale[r];
     const uint32_t q[4] = {v.x, v.y, v.z, v.w};
     float f[16];

@@ -70,7 +70,17 @@ constexpr int kOffK = 0;
 constexpr int kOffQR = kKStages * kKStageBytes;                       // the query's RoPE part, two boxes
 constexpr int kOffStaging = kOffQR + 2 * kBoxBytes;
 constexpr int kOffScale = kOffStaging + kStaging * kStgStride;
-constexpr int kRegion0 = kOffScale + kScaleSlots * kScaleBytes;
+// the query's latent boxes pass through the three tile stages that the row's first tile does not take (five
+// boxes a stage) and one box of their own, so that this tile is loaded while the query is converted
+constexpr int kOffQX = (kOffScale + kScaleSlots * kScaleBytes + 1023) / 1024 * 1024;
+constexpr int kOffQTop = kOffQX + kBoxBytes;           // uint32 [2][128]: each set's largest query magnitude per row
+constexpr int kRegion0 = kOffQTop + 2 * kH * 4;
+constexpr int kBoxesPerStage = kCodeBoxes + 1;
+__device__ __forceinline__ uint32_t q_box(uint32_t base, uint32_t first_tile, int i) {   // address of box i
+  if (i == kQBoxes - 1) return base + kOffQX;
+  return base + kOffK + (uint32_t)((first_tile + 1 + i / kBoxesPerStage) % kKStages) * kKStageBytes +
+         (uint32_t)(i % kBoxesPerStage) * kBoxBytes;
+}
 constexpr int kOffV = 0;
 constexpr int kOffPSlots = kVStages * kVStageBytes;
 constexpr int kOffEpi = kOffPSlots + kPSlots * kSlotStride;
@@ -91,7 +101,7 @@ constexpr int kOffWork = kOffAbort + 8;
 constexpr int kSmemUsed = kOffWork + 48;
 constexpr int kSmemBytes = kSmemUsed + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kQBoxes * kBoxBytes <= kKStages * kKStageBytes, "the query passes through the tile ring");
+static_assert(kQBoxes - 1 <= (kKStages - 1) * kBoxesPerStage, "the query passes through the tile ring");
 static_assert(kOffQR % 1024 == 0 && kOffPSlots % 1024 == 0 && kKStageBytes % 1024 == 0 && kSlotStride % 1024 == 0 &&
               kOffScale % 16 == 0 && kOffStaging % 16 == 0 && kOffBar % 8 == 0 && kOffWork % 8 == 0, "alignment");
 
@@ -214,6 +224,19 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
     if (warp == 0) {
       // ---- TMA producer: the warp looks up the pages of 32 tiles at a time and waits as a whole; lane 0
       // issues the loads
+      auto load_tile = [&](uint32_t i, int page) {   // tile i of this pair, into its (free) stage
+        if (lane == 0) {
+          const uint32_t s = i % kKStages, dst = base + kOffK + s * kKStageBytes;
+          ptx::mbar_arrive_expect_tx(bar(K_FULL + s), kKStageBytes + kScaleBytes);
+          // (an off-the-map page takes page 0's scales: its result is undefined, its reads are not)
+          ptx::bulk_load(base + kOffScale + (i % kScaleSlots) * kScaleBytes,
+                         p.scales + (size_t)(page < p.num_pages ? page : 0) * kTile, kScaleBytes, bar(K_FULL + s));
+          for (int j = 0; j < kCodeBoxes; ++j)
+            ptx::tma_load_2d(dst + j * kBoxBytes, &tm_codes, 128 * j, page * kTile, bar(K_FULL + s));
+          ptx::tma_load_2d(dst + kCodeBoxes * kBoxBytes, &tm_rope, 0, page * kTile, bar(K_FULL + s));
+        }
+        __syncwarp();
+      };
       uint32_t it = 0, seg = 0;
       bool ok = true, q_out = false;
       while (ok && next()) {
@@ -225,12 +248,13 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(bar(Q_LOADED), (kQBoxes + 2) * kBoxBytes);
           for (int i = 0; i < kQBoxes; ++i)
-            ptx::tma_load_2d(base + kOffK + i * kBoxBytes, &tm_q, 64 * (i >> 1), b * kH + 64 * (i & 1), bar(Q_LOADED));
+            ptx::tma_load_2d(q_box(base, it, i), &tm_q, 64 * (i >> 1), b * kH + 64 * (i & 1), bar(Q_LOADED));
           for (int i = 0; i < 2; ++i)
             ptx::tma_load_2d(base + kOffQR + i * kBoxBytes, &tm_q, kDC, b * kH + 64 * i, bar(Q_LOADED));
         }
         q_out = true;
-        // meanwhile the first tiles into L2 (a box a lane)
+        // meanwhile the first tile into its stage, and the next ones into L2 (a box a lane)
+        load_tile(it, __shfl_sync(0xffffffffu, pages, 0));
         const int pre = min(t_hi - t_lo, kKStages);
         const int pre_page = __shfl_sync(0xffffffffu, pages, lane / kCodeBoxes);
         if (lane < pre * kCodeBoxes) ptx::tma_prefetch_2d(&tm_codes, 128 * (lane % kCodeBoxes), pre_page * kTile);
@@ -242,23 +266,17 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           const uint32_t s = it % kKStages;
           if (t > t_lo && ((t - t_lo) & 31) == 0) pages = t + lane < t_hi ? page_at(b, t + lane, true) : 0;
           const int page = __shfl_sync(0xffffffffu, pages, (t - t_lo) & 31);
+          if (t == t_lo) continue;   // loaded above
           if (!(ok = wait_bar_warp(bar(K_EMPTY + s), ((it / kKStages) & 1u) ^ 1u, abort_addr, false))) break;
-          if (lane == 0) {
-            const uint32_t dst = base + kOffK + s * kKStageBytes;
-            ptx::mbar_arrive_expect_tx(bar(K_FULL + s), kKStageBytes + kScaleBytes);
-            // (an off-the-map page takes page 0's scales: its result is undefined, its reads are not)
-            ptx::bulk_load(base + kOffScale + (it % kScaleSlots) * kScaleBytes,
-                           p.scales + (size_t)(page < p.num_pages ? page : 0) * kTile, kScaleBytes, bar(K_FULL + s));
-            for (int j = 0; j < kCodeBoxes; ++j)
-              ptx::tma_load_2d(dst + j * kBoxBytes, &tm_codes, 128 * j, page * kTile, bar(K_FULL + s));
-            ptx::tma_load_2d(dst + kCodeBoxes * kBoxBytes, &tm_rope, 0, page * kTile, bar(K_FULL + s));
-          }
-          __syncwarp();
+          load_tile(it, page);
         }
       }
       // loads still in flight must land before the CTA may exit
       if (lane == 0) {
-        if (q_out) wait_bar(bar(Q_LOADED), seg & 1u, abort_addr, false, false);
+        if (q_out) {   // given up between the query's loads and the first tile's count
+          wait_bar(bar(Q_LOADED), seg & 1u, abort_addr, false, false);
+          ++it;
+        }
         for (uint32_t i = (it > (uint32_t)kKStages ? it - kKStages : 0); i < it; ++i)
           wait_bar(bar(K_FULL + i % kKStages), (i / kKStages) & 1u, abort_addr, false, false);
       }
@@ -332,30 +350,35 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
       bool ok = true;
       while (ok && next()) {
         const int L = vlen(b);
-        // ---- the row's query: q 2^t as two E4M3 terms into TMEM; each set finds the row's largest value
-        // and converts half of its columns
+        // ---- the row's query: q 2^t as two E4M3 terms into TMEM. Each set takes half of its columns; the
+        // row's largest value comes from both
         float q_unit = 0.f;   // 2^-t
         ok = wait_bar_warp(bar(Q_LOADED), seg & 1u, abort_addr, false);
+        uint32_t* q_top = reinterpret_cast<uint32_t*>(gbase + kOffQTop);
+        const int r = row & 63, rh = row >> 6;
         if (ok) {
-          const int r = row & 63, rh = row >> 6;
           uint32_t top = 0;   // the largest magnitude of the two halves of each word, as bf16 bits
 #pragma unroll 1
-          for (int cb = 0; cb < kDC / 64; ++cb) {
-            const uint32_t srow = base + kOffK + (uint32_t)(2 * cb + rh) * kBoxBytes + (uint32_t)r * 128u;
+          for (int cb = 4 * set; cb < 4 * set + 4; ++cb) {
+            const uint32_t srow = q_box(base, it, 2 * cb + rh) + (uint32_t)r * 128u;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const uint4 x = ptx::ld_shared_v4(srow + ((uint32_t)(k ^ (r & 7)) << 4));
               top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
             }
           }
+          q_top[set * kH + row] = max(top & 0xffffu, top >> 16);
+        }
+        ok = !ptx::named_bar_or(3, kGroup, !ok);   // all row warps meet here, and agree
+        if (ok) {
           // largest value < 2^(e - 126): 2^t = 2^(134 - e) brings it below 2^8 (e at least 8, so that 2^t is
           // a float); an infinite or NaN query has no finite scores
-          const int e = max((int)(max(top & 0xffffu, top >> 16) >> 7), 8);
+          const int e = max((int)(max(q_top[row], q_top[kH + row]) >> 7), 8);
           const float up = __uint_as_float((uint32_t)(261 - e) << 23);
           q_unit = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(e - 7) << 23);
 #pragma unroll 1
           for (int cb = 4 * set; cb < 4 * set + 4; ++cb) {
-            const uint32_t srow = base + kOffK + (uint32_t)(2 * cb + rh) * kBoxBytes + (uint32_t)r * 128u;
+            const uint32_t srow = q_box(base, it, 2 * cb + rh) + (uint32_t)r * 128u;
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -366,8 +389,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
                 uint32_t h0, l0, h1, l1;
                 split_e4m3x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up, &h0, &l0);
                 split_e4m3x2(__uint_as_float(w[j + 1] << 16) * up, __uint_as_float(w[j + 1] & 0xffff0000u) * up, &h1, &l1);
-                hi[2 * k + j / 2] = h0 | (h1 << 16);
-                lo[2 * k + j / 2] = l0 | (l1 << 16);
+                hi[2 * k + j / 2] = __byte_perm(h0, h1, 0x5410);
+                lo[2 * k + j / 2] = __byte_perm(l0, l1, 0x5410);
               }
             }
             ptx::tmem_st16(tmem + lane_off + 16u * cb, hi);
@@ -632,7 +655,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
         const uint8_t* src = lane_codes + (int64_t)(page < p.num_pages ? page : 0) * kTile * p.code_stride;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          cd[i] = page < p.num_pages ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(8 * i) * p.code_stride))
+          cd[i] = page < p.num_pages ? *reinterpret_cast<const uint4*>(src + (int64_t)(8 * i) * p.code_stride)
                                      : make_uint4(0u, 0u, 0u, 0u);
       };
       load_codes(next_page());

@@ -144,8 +144,8 @@ __host__ __device__ __forceinline__ int tiles_of(int L, int max_tiles) { return 
 // Tiles of work item b. Dense: the pages of sequence b, from its length. Sparse: the pages listed for row
 // b (`lens` is then the array of counts).
 template <bool kSparse>
-__device__ __forceinline__ int item_tiles(const int32_t* __restrict__ lens, int b, int max_tiles) {
-  const int L = __ldg(lens + b);
+__device__ __forceinline__ int item_tiles(const int32_t* lens, int b, int max_tiles) {
+  const int L = lens[b];
   if constexpr (kSparse) return min(max(L, 0), max_tiles);
   else return tiles_of(L, max_tiles);
 }
@@ -562,7 +562,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       const int vis = p.seqlens[seq] - (p.list_s_q - 1 - bb % p.list_s_q);
       w.table = p.block_table + (long long)seq * p.max_pages;
       w.list = p.page_list + (long long)bb * p.list_k;
-      w.pages_seen = vis > 0 ? (vis + kTile - 1) / kTile : 0;
+      w.pages_seen = vis > 0 ? (vis - 1) / kTile + 1 : 0;
       w.before = lo > 0 ? w.list[lo - 1] : -1;
       const int first = w.list[lo];
       w.page = w.lookup(first);

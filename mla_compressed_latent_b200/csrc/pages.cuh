@@ -12,7 +12,7 @@ namespace pages {
 // L - s_q + t + 1.
 __device__ __forceinline__ int visible_pages(int L, int s_q, int t) {
   const int vis = L - s_q + t + 1;
-  return vis > 0 ? (vis + 63) / 64 : 0;
+  return vis > 0 ? (vis - 1) / 64 + 1 : 0;
 }
 
 // =============================================================================================
@@ -72,9 +72,9 @@ constexpr int kKeyThreads = 640;   // most threads of a block
 // V: columns per piece (16 bytes of T, or 1 when a width is not a multiple of that); kCodes: 8-bit rows.
 template <typename T, int V, bool kCodes>
 __global__ void __launch_bounds__(kKeyThreads)
-page_keys_kernel(CacheView<T> cache, const int32_t* __restrict__ block_table, int max_pages,
-                                 const int32_t* __restrict__ seqlens, int s_q, int per_seq, int d_c, int d_r,
-                                 T* __restrict__ keys, int64_t key_stride) {
+page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
+                                 const int32_t* seqlens, int s_q, int per_seq, int d_c, int d_r,
+                                 T* keys, int64_t key_stride) {
   extern __shared__ float part[];   // [kKeyGroups][W]
   grid_dependency_wait();
   allow_dependents();
@@ -159,7 +159,7 @@ __device__ __forceinline__ int token_pages(const ScoreArgs& A, int v, bool may_r
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kScoreHeads)
-score_products_kernel(ScoreArgs A, const T* __restrict__ q, const T* __restrict__ keys, int64_t key_stride) {
+score_products_kernel(ScoreArgs A, const T* q, const T* keys, int64_t key_stride) {
   extern __shared__ float sm[];
   const int v = blockIdx.x, p0 = blockIdx.y * kScorePages, h0 = blockIdx.z * kScoreHeads;
   const int n = token_pages(A, v, threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0);
@@ -240,8 +240,8 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads)
-select_pages_kernel(const float* __restrict__ scores, int max_pages, const int32_t* __restrict__ seqlens, int s_q, int k,
-                    int n_first, int n_recent, int32_t* __restrict__ list, int32_t* __restrict__ counts) {
+select_pages_kernel(const float* scores, int max_pages, const int32_t* seqlens, int s_q, int k,
+                    int n_first, int n_recent, int32_t* list, int32_t* counts) {
   __shared__ int hist[256];
   __shared__ int s_digit, s_left;
   __shared__ int warp_gt[32], warp_eq[32];
@@ -264,7 +264,7 @@ select_pages_kernel(const float* __restrict__ scores, int max_pages, const int32
   const float* sc = scores + (int64_t)v * max_pages;
   auto rank_at = [&](int p) -> uint32_t {
     // the highest rank of a number is that of +inf: 0xff800000
-    return (p < n_first || p >= n - n_recent) ? 0xffffffffu : rank_of(__ldg(sc + p));
+    return (p < n_first || p >= n - n_recent) ? 0xffffffffu : rank_of(sc[p]);
   };
   uint32_t keep[kKeep];
 #pragma unroll
