@@ -308,25 +308,28 @@ def _need(dev: int, name: str, t: torch.Tensor, shape, dtype) -> int:
     return t.data_ptr()
 
 
-def _need_rows(dev: int, name: str, t: torch.Tensor, rows: int, width: int, dtype) -> None:
-    """A matrix of at least `rows` rows of `width` values laid end to end (rows may be strided)."""
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or \
-            (width > 1 and t.stride(1) != 1):
+def _need_rows(dev: int, name: str, t: torch.Tensor, rows: int, width: int, dtype):
+    """(data_ptr, elements between rows) of a matrix of at least `rows` rows of `width` values laid end to end."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2 or shape[0] < rows or shape[1] != width or \
+            (stride[1] != 1 and width > 1):
         _refuse(dev, name, t, dtype, f"at least {rows} rows of {width} values")
+    return t.data_ptr(), stride[0]
 
 
 def _cache_arg(dev: int, dims: Dims, cache, dtype):
     """The checked descriptor of a latent cache (LatentCache or LatentCacheFp8)."""
-    rows = cache.num_pages * 64
-    _need_rows(dev, "cache.rope", cache.rope, rows, dims.d_r, dtype)
+    n = cache.num_pages
+    rope, rope_stride = _need_rows(dev, "cache.rope", cache.rope, n * 64, dims.d_r, dtype)
     if isinstance(cache, LatentCacheFp8):
-        _need_rows(dev, "cache.codes", cache.codes, rows, dims.d_c, torch.uint8)
-        if cache.scales.dim() != 1 or cache.scales.shape[0] < rows:
-            raise ValueError(f"cache.scales: expected at least {rows} values, got {tuple(cache.scales.shape)}")
-        _need(dev, "cache.scales", cache.scales, cache.scales.shape, torch.float32)
-    else:
-        _need_rows(dev, "cache.latent", cache.latent, rows, dims.d_c, dtype)
-    return cache.c()
+        codes, code_stride = _need_rows(dev, "cache.codes", cache.codes, n * 64, dims.d_c, torch.uint8)
+        scales = cache.scales
+        if scales.dtype is not torch.float32 or scales.get_device() != dev or scales.dim() != 1 or \
+                scales.numel() < n * 64 or not scales.is_contiguous():
+            _refuse(dev, "cache.scales", scales, torch.float32, f"at least {n * 64} contiguous values")
+        return L.MlaLatentCacheFp8(codes, code_stride, scales.data_ptr(), rope, rope_stride, n)
+    latent, latent_stride = _need_rows(dev, "cache.latent", cache.latent, n * 64, dims.d_c, dtype)
+    return L.MlaLatentCache(latent, latent_stride, rope, rope_stride, n)
 
 
 def _table(dev: int, B: int, block_table, seqlens):
@@ -417,11 +420,11 @@ def mla_read_latent_fp8(dims: Dims, cache: LatentCacheFp8, block_table, row_offs
     table, max_pages, _ = _table(dev, B, block_table, None)
     off = _need(dev, "row_offsets", row_offsets, (B + 1,), torch.int32)
     pf = None if first is None else _need(dev, "first", first, (B,), torch.int32)
-    _need_rows(dev, "out", out, 1, _width(dims), out.dtype)
+    po, out_stride = _need_rows(dev, "out", out, 1, _width(dims), out.dtype)
     cc = _cache_arg(dev, dims, cache, out.dtype)
     d = dims.c()
     rc = lib.mla_read_latent_fp8(ctypes.byref(d), dt, B, ctypes.byref(cc), table, max_pages, pf, off, out.shape[0],
-                                 out.data_ptr(), out.stride(0), _stream_on(dev, stream))
+                                 po, out_stride, _stream_on(dev, stream))
     _check("mla_read_latent_fp8", rc)
     return out
 
@@ -434,12 +437,12 @@ def mla_update_page_keys(dims: Dims, cache, block_table, seqlens, s_q: int, keys
     dev = _current(keys)
     B = block_table.shape[0]
     table, max_pages, lens = _table(dev, B, block_table, seqlens)
-    _need_rows(dev, "keys", keys, cache.num_pages, _width(dims), keys.dtype)
+    pk, key_stride = _need_rows(dev, "keys", keys, cache.num_pages, _width(dims), keys.dtype)
     cc = _cache_arg(dev, dims, cache, keys.dtype)
     name = "mla_update_page_keys_fp8" if isinstance(cache, LatentCacheFp8) else "mla_update_page_keys"
     d = dims.c()
-    rc = getattr(lib, name)(ctypes.byref(d), dt, B, s_q, ctypes.byref(cc), table, max_pages, lens, keys.data_ptr(),
-                            keys.stride(0), _stream_on(dev, stream))
+    rc = getattr(lib, name)(ctypes.byref(d), dt, B, s_q, ctypes.byref(cc), table, max_pages, lens, pk, key_stride,
+                            _stream_on(dev, stream))
     _check(name, rc)
     return keys
 
@@ -454,14 +457,14 @@ def mla_score_pages(dims: Dims, q_abs, keys, block_table, seqlens, scores=None, 
     B, s_q = q_abs.shape[0], q_abs.shape[1]
     pq = _need(dev, "q_abs", q_abs, (B, s_q, dims.H, _width(dims)), q_abs.dtype)
     table, max_pages, lens = _table(dev, B, block_table, seqlens)
-    _need_rows(dev, "keys", keys, 1, _width(dims), q_abs.dtype)
+    pk, key_stride = _need_rows(dev, "keys", keys, 1, _width(dims), q_abs.dtype)
     if scores is None:
         scores = _new(dev, stream, torch.zeros, B, s_q, max_pages, dtype=torch.float32)
     ps = _need(dev, "scores", scores, (B, s_q, max_pages), torch.float32)
     d = dims.c()
     need = _bytes("mla_score_pages_workspace_size", dev, dims, dt, B, s_q, max_pages)
     workspace, ws, wsb = _space(dev, need, workspace, stream)
-    rc = lib.mla_score_pages(ctypes.byref(d), dt, B, s_q, pq, keys.data_ptr(), keys.stride(0), keys.shape[0], table,
+    rc = lib.mla_score_pages(ctypes.byref(d), dt, B, s_q, pq, pk, key_stride, keys.shape[0], table,
                              max_pages, lens, ps, ws, wsb, _stream_on(dev, stream))
     _check("mla_score_pages", rc)
     return scores
