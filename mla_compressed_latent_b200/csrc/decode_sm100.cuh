@@ -200,6 +200,27 @@ __host__ __device__ __forceinline__ int active_groups(int G, long long T) {
   }
 }
 
+// Whether no row (sequence) is cut. Dense: see whole_sequences. Sparse: rows are short, and a segment costs a
+// pair as much as kSegmentTiles tiles beyond its own (the query's load, the first tile's and the last one's
+// latency, the epilogue; about 15 us against 1.1 us a tile); a cut costs its parts besides (256 KB of fp32 each,
+// written and read again: about a tile's time for kPartsPerTile of them). So whole rows, dealt out
+// evenly, are taken unless their longest pair would work longer than all pairs on even shares of the
+// tiles. Measured, cut and whole: 124 rows of 4 pages 109 and 33 us; 16 of 16 47 and XX; 100 of 25 140 and XX; one row of 32
+// pages 25 us cut.
+constexpr int kSegmentTiles = 14, kPartsPerTile = 4;
+template <bool kSparse>
+__host__ __device__ __forceinline__ bool nothing_cut(int B, int groups, long long T, int max_tb) {
+  if constexpr (kSparse) {
+    const int G = active_groups<true>(groups, T);
+    const long long whole = (long long)((B + groups - 1) / groups) * (max_tb + kSegmentTiles);
+    const long long parts = G + (B < G ? B : G);
+    const long long cut = (T + G - 1) / G + (long long)kSegmentTiles * (B + G) / G + parts / kPartsPerTile;
+    return whole <= cut;
+  } else {
+    return whole_sequences(B, groups, T, max_tb);
+  }
+}
+
 // One warp: total tiles T, this pair's range, and the sequence holding its first tile. Lane l scans
 // sequences [l*per, (l+1)*per).
 template <bool kSparse>
@@ -225,13 +246,32 @@ __device__ void plan_range(const int32_t* lens, int B, int s_q, int max_tiles, i
   }
   const long long T = __shfl_sync(0xffffffffu, incl, 31);
   const long long excl = incl - local;
-  const int G = active_groups<kSparse>(npairs / s_q, T), grp = pair / s_q;
-  if (lane == 0) { out[4] = T; out[5] = (G > 0 && whole_sequences(B, G, T, max_tb)) ? 1 : 0; }
+  const int grp = pair / s_q;
+  const bool whole = npairs / s_q > 0 && nothing_cut<kSparse>(B, npairs / s_q, T, max_tb);
+  const int G = whole ? npairs / s_q : active_groups<kSparse>(npairs / s_q, T);
+  if (lane == 0) { out[4] = T; out[5] = whole ? 1 : 0; }
   if (grp >= G) {   // left over when s_q does not divide the pairs: no work
     if (lane == 0) { out[0] = 0; out[1] = 0; out[2] = 0; out[3] = B; }
     return;
   }
-  if (whole_sequences(B, G, T, max_tb)) {
+  if (kSparse && whole) {
+    // group g: rows [g B / G, (g + 1) B / G), none of them cut
+    const int lo = (int)((long long)grp * B / G), hi = (int)((long long)(grp + 1) * B / G);
+    auto before = [&](int x) -> long long {   // tiles of the rows before x (x in this lane's range)
+      long long off = excl;
+      for (int b = b0; b < x; ++b) off += item_tiles<kSparse>(lens, b, max_tiles);
+      return off;
+    };
+    if (lo == hi) {
+      if (lane == 0) { out[0] = 0; out[1] = 0; out[2] = 0; out[3] = B; }
+      return;
+    }
+    if (lo >= b0 && lo < b1) { out[0] = before(lo); out[2] = out[0]; out[3] = lo; }
+    if (hi >= b0 && hi < b1) out[1] = before(hi);
+    if (hi == B && lane == 0) out[1] = T;
+    return;
+  }
+  if (whole) {
     // group g: sequence g whole
     if (grp >= B) {
       if (lane == 0) { out[0] = 0; out[1] = 0; out[2] = 0; out[3] = B; }
@@ -1119,7 +1159,7 @@ merge_kernel(const int32_t* __restrict__ lens, int B, int s_q, int max_tiles, in
   }
   const long long T = local;
   const int G = active_groups<kSparse>(npairs / s_q, T);
-  if (T == 0 || G == 0 || whole_sequences(B, G, T, max_tb)) return;   // nothing was cut
+  if (T == 0 || G == 0 || nothing_cut<kSparse>(B, npairs / s_q, T, max_tb)) return;
   if constexpr (kSparse) {
     merge_rows(lens, B, max_tiles, G, T, (int)(blockIdx.y * gridDim.x + blockIdx.x), (int)(gridDim.x * gridDim.y), kMergeHeads,
                part_o, part_lse, o_lat, lse);

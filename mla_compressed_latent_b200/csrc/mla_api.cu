@@ -783,8 +783,8 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
                              : set_smem(mla::cache8::append_fp8_finish_kernel<__nv_bfloat16>, fs.smem)))
     return rc;
   float* part = reinterpret_cast<float*>(workspace);
-  // with few slices a row a warp is as quick to sum as to spread over a block, and there are rows enough
-  const bool rows_in_warps = ks <= 8 && n_tok >= 2 * num_sms() && N % 4 == 0 && dims->d_c <= 128 * mla::cache8::kRowChunks &&
+  // with rows enough and not too many slices a warp sums its row as quickly as a block would
+  const bool rows_in_warps = ks <= 24 && n_tok >= 2 * num_sms() && N % 4 == 0 && dims->d_c <= 128 * mla::cache8::kRowChunks &&
                              dims->d_r <= 64 * mla::cache8::kRowPairs;
   auto run = [&](auto zero) -> int {
     using T = decltype(zero);

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kKeyThreads)
 page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
                                  const int32_t* seqlens, int s_q, int per_seq, int d_c, int d_r,
                                  T* keys, int64_t key_stride) {
-  extern __shared__ float part[];   // [kKeyGroups][W]
+  extern __shared__ __align__(16) float part[];   // [kKeyGroups][W]
   grid_dependency_wait();
   allow_dependents();
   const int b = blockIdx.x / per_seq, i = blockIdx.x % per_seq;
@@ -117,8 +117,13 @@ page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
     for (int u = 0; u < 64 / kKeyGroups; ++u)
 #pragma unroll
       for (int k = 0; k < V; ++k) acc[k] += f[u][k];
+    if constexpr (V == 1) {
+      part[g * W + q] = acc[0];
+    } else {   // (W is a multiple of V here: 16-byte stores)
 #pragma unroll
-    for (int k = 0; k < V; ++k) part[g * W + q * V + k] = acc[k];
+      for (int k = 0; k < V; k += 4)
+        *reinterpret_cast<float4*>(part + g * W + q * V + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+    }
   }
   __syncthreads();
   T* dst = keys + (int64_t)page * key_stride;

@@ -33,8 +33,10 @@ constexpr int kH = 128;               // accumulator rows: heads, padded
 constexpr int kTile = 128;            // pages per product
 constexpr int kMaxPages = 512;        // pages per CTA: the accumulator's columns
 constexpr int kMaxChunks = 9;         // 64-column chunks of a row of up to 576 values
-constexpr int kStages = 10;
-constexpr int kAhead = 8;             // stages a thread's copies run ahead of what it has handed over
+// Key stages. Ten, eight of them in flight, for the long contexts of a few tokens; three for many tokens of at
+// most one tile of pages, so that two CTAs share an SM and one's latencies hide the other's (336
+// tokens of 11-18 pages: XX us with ten, XX us with three).
+constexpr int kLongStages = 10, kShortStages = 3;
 constexpr int kStageBytes = kTile * 128;
 constexpr int kQChunkBytes = kH * 128;
 constexpr int kWorkers = 256;         // threads of warps 0-7
@@ -43,13 +45,22 @@ constexpr int kMaxCluster = 8;
 constexpr int kQSlots = 3;            // chunks of q in shared memory
 constexpr int kMaxTiles = kMaxPages / kTile;
 constexpr int kOffRing = kQSlots * kQChunkBytes;
-constexpr int kOffStats = kOffRing + kStages * kStageBytes;            // float2 [cluster][2][kH]
-constexpr int kOffBar = kOffStats + kMaxCluster * 2 * kH * 8;
-enum Bar { FULL = 0, EMPTY = FULL + kStages, Q_FULL = EMPTY + kStages, Q_EMPTY = Q_FULL + kQSlots, DONE = Q_EMPTY + kQSlots, NUM_BARS };
-constexpr int kOffSlot = kOffBar + NUM_BARS * 8;
-constexpr int kSmemBytes = kOffSlot + 16 + 1024;   // + alignment slack of the dynamic base
-static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(4 * kMaxPages * 4 <= kOffRing, "the column sums fit the query's place");
+template <int kStages>
+struct Layout {
+  static constexpr int kAhead = kStages > 3 ? kStages - 2 : kStages - 1;   // stages a thread's copies run ahead of
+                                                                          // what it has handed over
+  static constexpr int kClusters = kStages == kShortStages ? 1 : kMaxCluster;
+  static constexpr int kTmemCols = kStages == kShortStages ? kTile : kMaxPages;
+  static constexpr int kOffStats = kOffRing + kStages * kStageBytes;   // float2 [cluster][2][kH]
+  static constexpr int kOffBar = kOffStats + kClusters * 2 * kH * 8;
+  static constexpr int FULL = 0, EMPTY = FULL + kStages, Q_FULL = EMPTY + kStages, Q_EMPTY = Q_FULL + kQSlots,
+                       DONE = Q_EMPTY + kQSlots, NUM_BARS = DONE + 1;
+  static constexpr int kOffSlot = kOffBar + NUM_BARS * 8;
+  static constexpr int kSmemBytes = kOffSlot + 16 + 1024;   // + alignment slack of the dynamic base
+};
+static_assert(Layout<kLongStages>::kSmemBytes <= 232448, "shared memory budget");
+static_assert(2 * (Layout<kShortStages>::kSmemBytes + 1024) <= 233472, "two CTAs to an SM");
 
 constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kH, kTile, false);
 
@@ -72,7 +83,13 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int kN>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory"); }
 
-__global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
+template <int kStages>
+__global__ void __launch_bounds__(kThreads, kStages == kShortStages ? 2 : 1)
+score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
+  using La = Layout<kStages>;
+  constexpr int FULL = La::FULL, EMPTY = La::EMPTY, Q_FULL = La::Q_FULL, Q_EMPTY = La::Q_EMPTY, DONE = La::DONE;
+  constexpr int kOffBar = La::kOffBar, kOffSlot = La::kOffSlot, kOffStats = La::kOffStats, kAhead = La::kAhead;
+  constexpr int kTiles = La::kTmemCols / kTile;   // most tiles of a CTA
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -92,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tm_q);
   }
-  if (warp == 8) { ptx::tmem_alloc(base + kOffSlot, 512); ptx::tmem_relinquish(); }
+  if (warp == 8) { ptx::tmem_alloc(base + kOffSlot, La::kTmemCols); ptx::tmem_relinquish(); }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -118,16 +135,16 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
     const int r0 = tid >> 3, piece = tid & 7;
     const uint32_t dst0 = base + kOffRing + (uint32_t)r0 * 128u + (((uint32_t)piece ^ ((uint32_t)r0 & 7u)) << 4);
     const int32_t* table = p.block_table + (int64_t)seq * p.max_pages + p0;
-    int pg[kMaxTiles][kU];   // the pages of this thread's rows, tile by tile; -1: zeros
+    int pg[kTiles][kU];   // the pages of this thread's rows, tile by tile; -1: zeros
 #pragma unroll
-    for (int t = 0; t < kMaxTiles; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int row = t * kTile + r0 + 32 * u;
         pg[t][u] = row < n ? table[row] : -1;
       }
 #pragma unroll
-    for (int t = 0; t < kMaxTiles; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
       for (int u = 0; u < kU; ++u)
         if (pg[t][u] < 0 || pg[t][u] >= p.num_pages) {
@@ -145,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
           const uint32_t dst = dst0 + (uint32_t)s * kStageBytes;
           const __nv_bfloat16* k0 = p.keys + (in ? col : 0);
 #pragma unroll
-          for (int t = 0; t < kMaxTiles; ++t) {
+          for (int t = 0; t < kTiles; ++t) {
             if (t != tile) continue;
 #pragma unroll
             for (int u = 0; u < kU; ++u)
@@ -310,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const __grid_constan
   __syncthreads();
   if (warp == 8) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc(tmem, La::kTmemCols);
   }
 }
 
@@ -331,7 +348,7 @@ inline int resident_clusters(int c, int num_sms) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(num_sms / c * c));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = Layout<kLongStages>::kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
@@ -340,7 +357,7 @@ inline int resident_clusters(int c, int num_sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, score_kernel, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, score_kernel<kLongStages>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = num_sms / c;
   }
@@ -355,7 +372,10 @@ inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const vo
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    if (cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(score_kernel<kLongStages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<kLongStages>::kSmemBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(score_kernel<kShortStages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<kShortStages>::kSmemBytes) != cudaSuccess)
       return MLA_ERR_CUDA;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
@@ -372,7 +392,8 @@ inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const vo
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * c));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  const bool many_short = rows > num_sms && max_pages <= kTile;
+  cfg.dynamicSmemBytes = many_short ? Layout<kShortStages>::kSmemBytes : Layout<kLongStages>::kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -383,7 +404,7 @@ inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const vo
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, score_kernel, tm_q, prm);
+  cudaLaunchKernelEx(&cfg, many_short ? score_kernel<kShortStages> : score_kernel<kLongStages>, tm_q, prm);
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

@@ -277,6 +277,8 @@ def _score_case(name, lens, s_q, seed, **over):
     ("dsv3_b64_l4096", [131072], 1, {}),
     ("dsv3_b64_l4096", [64 * 4200 + 9, 100], 1, {}),           # more pages than a cluster holds
     ("dsv3_b64_l4096", [777, 64 * 70], 2, {"H": 16}),          # fewer heads than a tile
+    ("dsv3_b64_l4096", list(range(1, 64 * 128, 130)), 3, {}),   # many tokens of one tile of pages: two CTAs an SM
+    ("dsv3_b64_l4096", [64 * 128] * 40 + [5, 64], 4, {"H": 24}),
     ("dsv3_b64_l4096", [777, 64 * 70], 1, {"H": 40, "d_c": 256, "d_r": 32}),
     ("dsv3_b64_l4096", [777], 1, {"H": 3, "d_c": 72, "d_r": 8}),
     ("dsv3_b64_l4096", [777, 64 * 9], 1, {"H": 192}),
@@ -434,6 +436,8 @@ SPARSE = [
     ([4096, 129, 2049, 64, 5000], 1, 20), ([700, 64 * 12 + 1], 2, 6), ([65, 130, 64 * 9], 4, 3),
     (list(np.random.default_rng(3).integers(1, 3000, 90)), 1, 13),
     (list(np.random.default_rng(4).integers(4, 3000, 40)), 4, 9),
+    # whole rows, several to a pair; rows of very different lengths, cut between pairs
+    (list(np.random.default_rng(5).integers(200, 700, 124)), 2, 4), ([300] * 80 + [6000] * 10, 1, 64),
 ]
 
 
