@@ -36,33 +36,43 @@ struct CacheView {
   int num_pages;
 };
 
+// V values of a row as they lie in memory: 16 bytes of T, or one value (V = 1), or V codes; and as fp32.
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
+__device__ __forceinline__ uint4 load_raw(const T* p) {
   if constexpr (V == 1) {
-    f[0] = ld(p);
+    return make_uint4(__float_as_uint(ld(p)), 0u, 0u, 0u);
   } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = ld(e + k);
+    return *reinterpret_cast<const uint4*>(p);
   }
 }
 template <int V>
-__device__ __forceinline__ void load_codes(const uint8_t* p, float sc, float (&f)[V]) {
+__device__ __forceinline__ uint4 load_raw_codes(const uint8_t* p) {
   static_assert(V == 4 || V == 8, "codes are read four or eight at a time");
-  uint32_t w[2] = {0u, 0u};
   if constexpr (V == 8) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
+    return make_uint4(v.x, v.y, 0u, 0u);
   } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
+    return make_uint4(*reinterpret_cast<const uint32_t*>(p), 0u, 0u, 0u);
   }
+}
+template <typename T, int V>
+__device__ __forceinline__ void add_raw(const uint4& v, float (&acc)[V]) {
+  if constexpr (V == 1) {
+    acc[0] += __uint_as_float(v.x);
+  } else {
+    const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] += ld(e + k);
+  }
+}
+template <int V>
+__device__ __forceinline__ void add_raw_codes(const uint4& v, float sc, float (&acc)[V]) {
+  const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
   for (int k = 0; k < V; k += 2) {
     const float2 x = cache8::e4m3x2_values(w[k >> 2] >> (16 * ((k >> 1) & 1)) & 0xffffu);
-    f[k] = x.x * sc;
-    f[k + 1] = x.y * sc;
+    acc[k] += x.x * sc;
+    acc[k + 1] += x.y * sc;
   }
 }
 
@@ -71,7 +81,7 @@ constexpr int kKeyThreads = 640;   // most threads of a block
 
 // V: columns per piece (16 bytes of T, or 1 when a width is not a multiple of that); kCodes: 8-bit rows.
 template <typename T, int V, bool kCodes>
-__global__ void __launch_bounds__(kKeyThreads)
+__global__ void __launch_bounds__(kKeyThreads, 2)
 page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
                                  const int32_t* seqlens, int s_q, int per_seq, int d_c, int d_r,
                                  T* keys, int64_t key_stride) {
@@ -97,26 +107,40 @@ page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
   const int W = d_c + d_r, Q = W / V, qc = d_c / V;
   for (int it = threadIdx.x; it < Q * kKeyGroups; it += blockDim.x) {
     const int q = it % Q, g = it / Q;
-    // all of the thread's rows are loaded before the first is added
-    float f[64 / kKeyGroups][V];
-#pragma unroll
-    for (int u = 0; u < 64 / kKeyGroups; ++u) {
-      const int r = g + u * kKeyGroups;
-      const int64_t row = (int64_t)page * 64 + r;
-#pragma unroll
-      for (int k = 0; k < V; ++k) f[u][k] = 0.f;
-      if (r >= n) continue;
-      if (q >= qc) load_vec<T, V>(cache.rope + row * cache.rope_stride + (q - qc) * V, f[u]);
-      else if constexpr (kCodes) load_codes<V>(cache.codes + row * cache.code_stride + q * V, cache.scales[row], f[u]);
-      else load_vec<T, V>(cache.latent + row * cache.latent_stride + q * V, f[u]);
-    }
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    constexpr int kBatch = 4;   // rows loaded before the first is added
+#pragma unroll 1
+    for (int r0 = g; r0 < n; r0 += kBatch * kKeyGroups) {
+      uint4 raw[kBatch];
+      float sc[kBatch];
 #pragma unroll
-    for (int u = 0; u < 64 / kKeyGroups; ++u)
+      for (int u = 0; u < kBatch; ++u) {
+        const int r = r0 + u * kKeyGroups;
+        const int64_t row = (int64_t)page * 64 + r;
+        raw[u] = make_uint4(0u, 0u, 0u, 0u);
+        sc[u] = 0.f;
+        if (r >= n) continue;
+        if (q >= qc) {
+          raw[u] = load_raw<T, V>(cache.rope + row * cache.rope_stride + (q - qc) * V);
+        } else if constexpr (kCodes) {
+          raw[u] = load_raw_codes<V>(cache.codes + row * cache.code_stride + q * V);
+          sc[u] = cache.scales[row];
+        } else {
+          raw[u] = load_raw<T, V>(cache.latent + row * cache.latent_stride + q * V);
+        }
+      }
 #pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] += f[u][k];
+      for (int u = 0; u < kBatch; ++u) {
+        if constexpr (kCodes) {
+          if (q < qc) add_raw_codes<V>(raw[u], sc[u], acc);
+          else add_raw<T, V>(raw[u], acc);
+        } else {
+          add_raw<T, V>(raw[u], acc);
+        }
+      }
+    }
     if constexpr (V == 1) {
       part[g * W + q] = acc[0];
     } else {   // (W is a multiple of V here: 16-byte stores)
