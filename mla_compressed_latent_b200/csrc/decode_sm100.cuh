@@ -205,8 +205,8 @@ __host__ __device__ __forceinline__ int active_groups(int G, long long T) {
 // latency, the epilogue; about 15 us against 1.1 us a tile); a cut costs its parts besides (256 KB of fp32 each,
 // written and read again: about a tile's time for kPartsPerTile of them). So whole rows, dealt out
 // evenly, are taken unless their longest pair would work longer than all pairs on even shares of the
-// tiles. Measured, cut and whole: 124 rows of 4 pages 109 and 33 us; 16 of 16 47 and XX; 100 of 25 140 and XX; one row of 32
-// pages 25 us cut.
+// tiles. Measured, cut and whole: 124 rows of 4 pages 109 and 33 us, 16 of 16 47 and 32 us, 100 of 25 140
+// and 74 us, 48 of 44 (8-bit) 104 and 68 us; one row of 32 pages 25 us cut.
 constexpr int kSegmentTiles = 14, kPartsPerTile = 4;
 template <bool kSparse>
 __host__ __device__ __forceinline__ bool nothing_cut(int B, int groups, long long T, int max_tb) {

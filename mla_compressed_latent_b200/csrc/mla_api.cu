@@ -729,7 +729,7 @@ namespace {
 // How the 8-bit append projects. With many tokens the projection is bound by what L2 delivers (about 9.5
 // TB/s to all SMs, measured), so it takes the tile that moves the fewest bytes per product: 256 features x 256
 // tokens, all 512 accumulator columns, 64 KB a K chunk of 64 (4096 tokens, C = 7168: 64 us with tiles of 128 x
-// 128, 49 us with 384 x 128, XX us so). K is cut so that the tiles fill the SMs. Fewer tokens: the split of a1.
+// 128, 49 us with 384 x 128, 41 us so). K is cut so that the tiles fill the SMs. Fewer tokens: the split of a1.
 struct AppendPlan {
   bool tc, wide;
   int ks;
@@ -808,8 +808,9 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
     }
     if (rows_in_warps) {
       const int blocks = std::min((n_tok + mla::cache8::kRowWarps - 1) / mla::cache8::kRowWarps, 4 * num_sms());
-      mla::launch_pdl(dims->d_c <= 512 ? mla::cache8::append_fp8_rows_kernel<T, 4>
-                                       : mla::cache8::append_fp8_rows_kernel<T, mla::cache8::kRowChunks>,
+      mla::launch_pdl(dims->d_c <= 512 && dims->d_r <= 64
+                          ? mla::cache8::append_fp8_rows_kernel<T, 4, 1>
+                          : mla::cache8::append_fp8_rows_kernel<T, mla::cache8::kRowChunks, mla::cache8::kRowPairs>,
                       dim3(blocks),
                       dim3(32 * mla::cache8::kRowWarps), 0, st, (const float*)part, ks, n_tok, s_q, dims->d_c, dims->d_r,
                       (const T*)gamma, dims->rms_eps, dims->rope_base, seqlens, block_table, max_pages,

@@ -16,8 +16,10 @@
 // the accumulator into masses; warp 8 loads q by TMA and issues the products. The column chunks are the
 // outer loop and the page tiles the inner one: all tiles' accumulators live at once, so only the chunk of q
 // at hand has to be in shared memory and ten stages (160 KB, eight of them in flight) are left for
-// the keys. What bounds a long context is how many key bytes are in flight: with q resident (64 KB of
-// stages) 8 sequences of 16K-128K positions took 33 us, XX us so.
+// the keys. 8 sequences of 16K-128K positions, 2 tokens each: 33 us with q resident, 64 KB of stages and
+// clusters of powers of two, 23 us so (6 CTAs a token); the copies' issue (16 KB in 250 ns), the two
+// passes over the accumulator and the cluster's exchange share that time. 64 sequences of 4096 positions, a token
+// each: 12 us, latency.
 #pragma once
 
 #include "common.cuh"
@@ -35,7 +37,7 @@ constexpr int kMaxPages = 512;        // pages per CTA: the accumulator's column
 constexpr int kMaxChunks = 9;         // 64-column chunks of a row of up to 576 values
 // Key stages. Ten, eight of them in flight, for the long contexts of a few tokens; three for many tokens of at
 // most one tile of pages, so that two CTAs share an SM and one's latencies hide the other's (336
-// tokens of 11-18 pages: XX us with ten, XX us with three).
+// tokens of 11-18 pages: 33 us with ten, 21 us with three).
 constexpr int kLongStages = 10, kShortStages = 3;
 constexpr int kStageBytes = kTile * 128;
 constexpr int kQChunkBytes = kH * 128;
