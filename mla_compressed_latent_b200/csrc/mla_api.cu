@@ -248,7 +248,7 @@ MLA_API int mla_test_set_two_launches(int on) {
 #endif
 
 const char* mla_build_info(void) {
-  return "libmla: sm_100a; kernels: simt (fp32/bf16 all steps), sm100 absorbed decode, GQLA grouped decode and per-head projections (tcgen05/TMA)";
+  return "libmla: sm_100a; kernels: simt (fp32/bf16 all steps), sm100 absorbed decode (dense and over selected pages, 16- and 8-bit), page scores, GQLA grouped decode and per-head projections (tcgen05/TMA)";
 }
 
 int mla_check_status(void* stream) {

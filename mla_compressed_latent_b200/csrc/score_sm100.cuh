@@ -114,6 +114,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
   if (warp == 8) { ptx::tmem_alloc(base + kOffSlot, La::kTmemCols); ptx::tmem_relinquish(); }
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::cluster_arrive();   // waited for before the first store into another CTA: by then it has started
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + kOffSlot);
   grid_dependency_wait();
@@ -221,6 +222,8 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
       l = l * ptx::ex2_approx((m - mt) * s2) + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
       m = mt;
     }
+    __syncwarp();
+    ptx::cluster_wait();
     for (int r = 0; r < csize; ++r) {
       const uint32_t at = ptx::map_to_cta(base + kOffStats + (uint32_t)(((int)rank * 2 + half) * kH + head) * 8u, (uint32_t)r);
       ptx::st_cluster_f32(at, m);
@@ -276,6 +279,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
       gemm::wait(bar(DONE), 0);
     }
     __syncwarp();
+    ptx::cluster_wait();
   }
   ptx::tc_fence_before();
   ptx::cluster_sync();   // every CTA's statistics are in place
