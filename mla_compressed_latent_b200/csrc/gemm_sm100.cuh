@@ -34,7 +34,7 @@ struct Params {
   int M, K;                // output features per head, reduction length per head (K % 64 == 0)
   int n_tok;               // rows of X
   int chunks_per_split;    // K chunks (of 64) per blockIdx.z
-  int tn;                  // tokens per CTA = MMA N: 32, 64, 128 or 256
+  int tn;                  // tokens per CTA = MMA N: 32, 64 or 128
   int stages;              // ring depth, 1..kMaxStages
   // mode 0: bf16 Y[tok * y_tok_stride + h * y_head_stride + m]
   // mode 1: fp32 part[(split * n_tok + tok) * M + m]   (one head)
@@ -424,7 +424,6 @@ struct Problem {
   bool a_kmajor = false;     // w is [H * M, K] (each head's weight transposed), read K-major
   bool x_shared = false;     // x is [n_tok, K], the same row for every head
   int m_per_cta = 1;         // m-tiles per CTA (1..4; more than 1 needs MN-major weights, no w2)
-  int tokens = 0;            // tokens per CTA (32, 64, 128 or 256; 0: by the token count, at most 128)
 };
 
 constexpr int kSmemMax = 232448;   // 227 KB per CTA
@@ -458,7 +457,7 @@ inline int prepare(const Problem& pr, Params p, int max_stages, Prepared* out) {
   p.K = pr.K;
   p.n_tok = pr.n_tok;
   p.H = pr.H;
-  p.tn = pr.tokens ? pr.tokens : tokens_per_cta(pr.n_tok);
+  p.tn = tokens_per_cta(pr.n_tok);
   const int m_tiles = (pr.M + kBM - 1) / kBM;
   if (pr.m_per_cta < 1 || pr.m_per_cta > 4 || (pr.m_per_cta > 1 && (two || pr.a_kmajor))) return MLA_ERR_UNSUPPORTED;
   p.m_sub = std::min({pr.m_per_cta, m_tiles, 512 / p.tn});   // the accumulators fit TMEM's 512 columns

@@ -17,6 +17,7 @@
 #include "gqla_sm100.cuh"
 #include "cache8.cuh"
 #include "decode8_sm100.cuh"
+#include "gemm_pair_sm100.cuh"
 #include "pages.cuh"
 #include "score_sm100.cuh"
 
@@ -726,23 +727,20 @@ int latent_cache_args(const mla_dims_t* dims, int32_t dtype, const mla_latent_ca
 }  // namespace
 
 namespace {
-// How the 8-bit append projects. With many tokens the projection is bound by what L2 delivers (about 9.5
-// TB/s to all SMs, measured), so it takes the tile that moves the fewest bytes per product: 256 features x 256
-// tokens, all 512 accumulator columns, 64 KB a K chunk of 64 (4096 tokens, C = 7168: 64 us with tiles of 128 x
-// 128, 49 us with 384 x 128, 41 us so). K is cut so that the tiles fill the SMs. Fewer tokens: the split of a1.
+// How the 8-bit append projects. With many tokens the projection is bound by what L2 delivers and goes to the
+// pairs of SMs (gemm_pair_sm100.cuh); with fewer a pair's 512 tokens leave too few tiles, and the split of a1
+// is as good or better. C = 7168 and 2048, the whole append: 500 tokens 21.5 and 18.0 us by pairs, 21.0 and 18.0 by
+// a1's; 600 22.9 and 18.2, 22.1 and 16.2; 800 23.4 and 16.9, 24.8 and 17.5; 2048 28.2 and 20.2, 56.5 and 24.9.
 struct AppendPlan {
-  bool tc, wide;
+  bool tc, pair;
   int ks;
 };
-constexpr int kWideTokens = 512;   // tokens from which the wide tile is taken
+constexpr int kPairTokens = 640;   // tokens from which the pairs are taken
 AppendPlan append_fp8_plan(int32_t dtype, int n_tok, int C, int N) {
   AppendPlan a{append_on_tc(dtype, C, N), false, 0};
-  a.wide = a.tc && n_tok >= kWideTokens;
-  if (a.wide) {
-    const int ctas = ((N + 127) / 128 + 1) / 2 * ((n_tok + 255) / 256), chunks = C / mla::gemm::kBK;
-    const int ks = std::max(1, std::min(num_sms() / ctas, chunks));
-    const int per = (chunks + ks - 1) / ks;
-    a.ks = (chunks + per - 1) / per;
+  a.pair = a.tc && n_tok >= kPairTokens;
+  if (a.pair) {
+    a.ks = mla::gemm_pair::plan_splits(N, C, n_tok, num_sms());
   } else {
     a.ks = a.tc ? append_tc_splits(n_tok, C, N) : append_ksplit(n_tok, C, N);
   }
@@ -788,17 +786,14 @@ int mla_append_cache_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B, int32
                              dims->d_r <= 64 * mla::cache8::kRowPairs;
   auto run = [&](auto zero) -> int {
     using T = decltype(zero);
-    if (tc) {
+    if (plan.pair) {
+      if (int e = mla::gemm_pair::run(w_dkv_kr, x, C, N, n_tok, ks, part, st)) return e;
+    } else if (tc) {
       mla::gemm::Params p{};
       p.mode = 1;
       p.part = part;
       p.w_early = 1;
-      mla::gemm::Problem pr = with_sms({w_dkv_kr, x, 1, C, N, n_tok, ks});
-      if (plan.wide) {
-        pr.m_per_cta = 2;
-        pr.tokens = 256;
-      }
-      if (int e = mla::gemm::run(pr, p, st)) return e;
+      if (int e = mla::gemm::run(with_sms({w_dkv_kr, x, 1, C, N, n_tok, ks}), p, st)) return e;
     } else {
       const int k_chunk = ((C + ks - 1) / ks + 63) / 64 * 64;
       dim3 grid((N + mla::simt::PROJ_COLS - 1) / mla::simt::PROJ_COLS,

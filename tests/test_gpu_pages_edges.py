@@ -270,3 +270,37 @@ def test_two_streams_at_once():
     for i, h in enumerate((None, held)):
         for o, l in got[i]:
             _check_sparse(case, *lists[i], h, o, l)
+
+
+@pytest.mark.parametrize("d_c,d_r,C", [(512, 64, 320), (144, 16, 64), (208, 48, 704), (256, 8, 7168), (16, 8, 128)])
+@pytest.mark.parametrize("n_tok", [512, 513, 767, 1025])
+def test_append_fp8_of_many_tokens_at_odd_widths(d_c, d_r, C, n_tok):
+    """Tiles whose features or tokens end inside them, one to many K chunks (the split of K included)."""
+    g = torch.Generator().manual_seed(n_tok + C)
+    x = torch.randn(1, n_tok, C, generator=g).bfloat16()
+    w = (torch.randn(C, d_c + d_r, generator=g) * C ** -0.5).bfloat16()
+    seqlen, pages = n_tok + 5, n_tok // 64 + 2
+    table = torch.randperm(pages + 3, generator=g)[:pages].to(torch.int32)
+    rows = (pages + 3) * 64
+    codes = torch.full((rows, d_c), 9, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows,), -2.0, device="cuda")
+    rope = torch.full((rows, d_r), 3.0, dtype=torch.bfloat16, device="cuda")
+    dims = Dims(8, 64, d_r, d_c, 64)
+    ops.mla_append_cache_fp8(dims, x.cuda(), w.cuda(), None, torch.tensor([seqlen], dtype=torch.int32).cuda(),
+                             table[None].cuda(), LatentCacheFp8(codes, scales, rope, pages + 3))
+    ok()
+    pos = np.arange(5, seqlen)
+    at = table.numpy()[pos // 64].astype(np.int64) * 64 + pos % 64
+    c, kr = O.latent_rows(x[0].double().numpy(), w[:, :d_c].double().numpy(), w[:, d_c:].double().numpy(), pos, None,
+                          dims.rms_eps, dims.rope_base)
+    got_s = scales.cpu().numpy().astype(np.float64)[at]
+    got = F.e4m3_decode(codes.cpu().numpy()[at])
+    top = np.abs(c).max(1)
+    slack = 2.0 ** -13   # as in test_append_fp8
+    assert np.all(np.abs(got_s - top / 448) <= slack * top / 448)
+    bar = np.maximum(2.0 ** -4 * np.abs(c), 2.0 ** -10 * got_s[:, None]) + 2 * slack * top[:, None]
+    assert np.all(np.abs(got * got_s[:, None] - c) <= bar)
+    assert np.all(np.abs(_f64(rope)[at] - kr) <= 2.0 ** -8 * np.abs(kr) + slack * max(1.0, np.abs(kr).max()))
+    keep = torch.ones(rows, dtype=torch.bool)
+    keep[torch.from_numpy(at)] = False
+    assert bool((codes.cpu()[keep] == 9).all() and (scales.cpu()[keep] == -2).all() and (rope.cpu()[keep] == 3).all())
