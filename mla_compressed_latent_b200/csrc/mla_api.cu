@@ -727,7 +727,7 @@ int latent_cache_args(const mla_dims_t* dims, int32_t dtype, const mla_latent_ca
 }  // namespace
 
 namespace {
-// How the 8-bit append projects. With many tokens the projection is bound by what L2 delivers and goes to the
+// How the 8-bit append projects. With many tokens the projection is bound by what L2 delivers, and goes to the
 // pairs of SMs (gemm_pair_sm100.cuh); with fewer a pair's 512 tokens leave too few tiles, and the split of a1
 // is as good or better. C = 7168 and 2048, the whole append: 500 tokens 21.5 and 18.0 us by pairs, 21.0 and 18.0 by
 // a1's; 600 22.9 and 18.2, 22.1 and 16.2; 800 23.4 and 16.9, 24.8 and 17.5; 2048 28.2 and 20.2, 56.5 and 24.9.
