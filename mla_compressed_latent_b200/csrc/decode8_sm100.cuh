@@ -24,7 +24,7 @@
 // M >= max_j x_j + E - 14 and 2^E above the tile's scales, so that w = e s stays below 2^14; l sums the
 // same e, and O / l and M + log2 l need no correction.
 //
-// 64 rows of 40 pages (73 MB of codes, scales and keys, 54 GFLOP with the second term not counted): 67-70 us, where a
+// 64 rows of 40 pages (105 MB of codes, scales and keys, 46 GFLOP with the second term not counted): 67-70 us, where a
 // dequantising pass and the 16-bit decode took 124 us and attended rows rounded to bf16. A tile takes about
 // 1650 cycles at 1.55 GHz: its 36 S MMAs run at 43 cycles each beside the loads and the softmax (34
 // alone), and the widening's 64 KB of stores share the output CTA's shared memory with the MMAs' reads. About
