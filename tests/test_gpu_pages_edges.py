@@ -304,3 +304,68 @@ def test_append_fp8_of_many_tokens_at_odd_widths(d_c, d_r, C, n_tok):
     keep = torch.ones(rows, dtype=torch.bool)
     keep[torch.from_numpy(at)] = False
     assert bool((codes.cpu()[keep] == 9).all() and (scales.cpu()[keep] == -2).all() and (rope.cpu()[keep] == 3).all())
+
+
+def test_append_fp8_of_many_tokens_captured_and_on_two_streams():
+    """An append of many tokens and one of a step, eagerly, on two streams at once, and replayed from a graph: the
+    same bytes each time (no sum's order depends on the launch)."""
+    g = torch.Generator().manual_seed(3)
+    n, C, dims = 1600, 512, Dims(128, 128, 64, 512, 128)
+    x = torch.randn(2, n // 2, C, generator=g).bfloat16().cuda()
+    w = (torch.randn(C, 576, generator=g) * C ** -0.5).bfloat16().cuda()
+    pages = n // 64 + 2
+    table = torch.randperm(pages, generator=g)[:2 * (pages // 2)].to(torch.int32).view(2, -1).cuda()
+    lens = torch.tensor([n // 2, n // 2 + 9], dtype=torch.int32).cuda()
+
+    def cache():
+        return LatentCacheFp8(torch.zeros(pages * 64, 512, dtype=torch.uint8, device="cuda"),
+                              torch.zeros(pages * 64, device="cuda"),
+                              torch.zeros(pages * 64, 64, dtype=torch.bfloat16, device="cuda"), pages)
+
+    first, small = torch.ones(2, dtype=torch.int32).cuda(), x[:, :1].contiguous()
+
+    def call(c, stream=None):   # many tokens, then a step's
+        ops.mla_append_cache_fp8(dims, x, w, None, lens, table, c, stream=stream)
+        ops.mla_append_cache_fp8(dims, small, w, None, first, table, c, stream=stream)
+
+    eager, caches = cache(), [cache() for _ in range(3)]
+    call(eager)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for st, c in zip(streams, caches):
+            call(c, st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(caches[2])
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    ok()
+    for c in caches:
+        assert torch.equal(c.codes, eager.codes) and torch.equal(c.scales, eager.scales) and torch.equal(c.rope, eager.rope)
+
+
+def test_append_fp8_of_more_tokens_than_one_wave():
+    g = torch.Generator().manual_seed(4)
+    n, C, d_c, d_r = 16421, 128, 512, 64
+    dims = Dims(128, 128, d_r, d_c, 128)
+    x = torch.randn(1, n, C, generator=g).bfloat16()
+    w = (torch.randn(C, d_c + d_r, generator=g) * C ** -0.5).bfloat16()
+    pages = n // 64 + 1
+    table = torch.randperm(pages, generator=g).to(torch.int32)
+    codes = torch.zeros(pages * 64, d_c, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(pages * 64, device="cuda")
+    rope = torch.zeros(pages * 64, d_r, dtype=torch.bfloat16, device="cuda")
+    ops.mla_append_cache_fp8(dims, x.cuda(), w.cuda(), None, torch.tensor([n], dtype=torch.int32).cuda(), table[None].cuda(),
+                             LatentCacheFp8(codes, scales, rope, pages))
+    ok()
+    pos = np.arange(n)
+    at = table.numpy()[pos // 64].astype(np.int64) * 64 + pos % 64
+    c, kr = O.latent_rows(x[0].double().numpy(), w[:, :d_c].double().numpy(), w[:, d_c:].double().numpy(), pos, None,
+                          dims.rms_eps, dims.rope_base)
+    got_s = scales.cpu().numpy().astype(np.float64)[at]
+    top, slack = np.abs(c).max(1), 2.0 ** -13   # as in test_append_fp8
+    bar = np.maximum(2.0 ** -4 * np.abs(c), 2.0 ** -10 * got_s[:, None]) + 2 * slack * top[:, None]
+    assert np.all(np.abs(F.e4m3_decode(codes.cpu().numpy()[at]) * got_s[:, None] - c) <= bar)
+    assert np.all(np.abs(_f64(rope)[at] - kr) <= 2.0 ** -8 * np.abs(kr) + slack * max(1.0, np.abs(kr).max()))
