@@ -6,8 +6,9 @@
 // the heads of one page, so a token needs all of u before it can write anything. u never leaves the
 // SM: the 128 heads are the M rows of the product and pages its N columns, and an accumulator of 128
 // lanes x 512 columns is exactly the tensor memory of one SM. A cluster of 1 to 8 CTAs takes one
-// token, up to 512 pages each; the CTAs swap each head's running maximum and sum through
-// distributed shared memory, and read their u a second time to sum the masses over the heads.
+// token, up to 512 pages each. A CTA puts e = exp(u - its head's maximum) in u's place, the CTAs swap each
+// head's maximum and sum through distributed shared memory, and e times one factor a head is then summed
+// over the heads: each exponential is computed once.
 // Bound: q (128 rows) and the keys, read once per token (keys of one sequence come from L2 after the first
 // token); 2 · 128 · (d_c + d_r) operations a page.
 //
@@ -15,11 +16,11 @@
 // thread with asynchronous copies into 128-byte swizzled stages of 128 pages x 64 columns), then turn
 // the accumulator into masses; warp 8 loads q by TMA and issues the products. The column chunks are the
 // outer loop and the page tiles the inner one: all tiles' accumulators live at once, so only the chunk of q
-// at hand has to be in shared memory and ten stages (160 KB, eight of them in flight) are left for
-// the keys. 8 sequences of 16K-128K positions, 2 tokens each: 33 us with q resident, 64 KB of stages and
-// clusters of powers of two, 23 us so (6 CTAs a token); the copies' issue (16 KB in 250 ns), the two
-// passes over the accumulator and the cluster's exchange share that time. 64 sequences of 4096 positions, a token
-// each: 12 us, latency.
+// at hand has to be in shared memory. 8 sequences of 16K-128K positions, 2 tokens each (6 CTAs a token; from
+// the start of the longest's): page table 3.4 us, keys gathered 13.5 (27 stages, 16 KB in 0.35 us whatever is in
+// flight), products done 14.6, exponentials 16.6, exchanged 17.7, summed 20.4; 33 us with q resident and
+// clusters of powers of two, 23 us with every exponential computed twice and eight stages ahead. 64 sequences of
+// 4096 positions, a token each: 9.2 us (10.7 with three chunks of q), latency.
 #pragma once
 
 #include "common.cuh"
@@ -35,25 +36,25 @@ constexpr int kH = 128;               // accumulator rows: heads, padded
 constexpr int kTile = 128;            // pages per product
 constexpr int kMaxPages = 512;        // pages per CTA: the accumulator's columns
 constexpr int kMaxChunks = 9;         // 64-column chunks of a row of up to 576 values
-// Key stages. Ten, eight of them in flight, for the long contexts of a few tokens; three for many tokens of at
-// most one tile of pages, so that two CTAs share an SM and one's latencies hide the other's (336
-// tokens of 11-18 pages: 33 us with ten, 21 us with three).
-constexpr int kLongStages = 10, kShortStages = 3;
+// Key stages and chunks of q in shared memory. Six of each: the copies' issue bounds the gather, not what is in
+// flight (two to eight stages ahead bring a long context's keys in the same time, but what is handed over late
+// delays the products), and with one tile of pages the query is the larger part of what a CTA loads. For
+// many tokens of at most one tile, three of each, so that two CTAs share an SM and one's latencies hide the
+// other's (336 tokens of 11-18 pages: 33 us with one CTA, 21 us with two).
+constexpr int kStagesOne = 6, kStagesTwo = 3;
 constexpr int kStageBytes = kTile * 128;
 constexpr int kQChunkBytes = kH * 128;
 constexpr int kWorkers = 256;         // threads of warps 0-7
 constexpr int kThreads = kWorkers + 32;
 constexpr int kMaxCluster = 8;
-constexpr int kQSlots = 3;            // chunks of q in shared memory
-constexpr int kMaxTiles = kMaxPages / kTile;
-constexpr int kOffRing = kQSlots * kQChunkBytes;
-static_assert(4 * kMaxPages * 4 <= kOffRing, "the column sums fit the query's place");
 template <int kStages>
 struct Layout {
-  static constexpr int kAhead = kStages > 3 ? kStages - 2 : kStages - 1;   // stages a thread's copies run ahead of
-                                                                          // what it has handed over
-  static constexpr int kClusters = kStages == kShortStages ? 1 : kMaxCluster;
-  static constexpr int kTmemCols = kStages == kShortStages ? kTile : kMaxPages;
+  static constexpr int kAhead = kStages > 3 ? 3 : 2;   // stages a thread's copies run ahead of what it has handed over
+  static constexpr int kQSlots = kStages;
+  static constexpr int kOffRing = kQSlots * kQChunkBytes;
+  static constexpr int kClusters = kStages == kStagesTwo ? 1 : kMaxCluster;
+  static constexpr int kTmemCols = kStages == kStagesTwo ? kTile : kMaxPages;
+  static_assert(4 * kMaxPages * 4 <= kOffRing, "the column sums fit the query's place");
   static constexpr int kOffStats = kOffRing + kStages * kStageBytes;   // float2 [cluster][2][kH]
   static constexpr int kOffBar = kOffStats + kClusters * 2 * kH * 8;
   static constexpr int FULL = 0, EMPTY = FULL + kStages, Q_FULL = EMPTY + kStages, Q_EMPTY = Q_FULL + kQSlots,
@@ -61,8 +62,8 @@ struct Layout {
   static constexpr int kOffSlot = kOffBar + NUM_BARS * 8;
   static constexpr int kSmemBytes = kOffSlot + 16 + 1024;   // + alignment slack of the dynamic base
 };
-static_assert(Layout<kLongStages>::kSmemBytes <= 232448, "shared memory budget");
-static_assert(2 * (Layout<kShortStages>::kSmemBytes + 1024) <= 233472, "two CTAs to an SM");
+static_assert(Layout<kStagesOne>::kSmemBytes <= 232448, "shared memory budget");
+static_assert(2 * (Layout<kStagesTwo>::kSmemBytes + 1024) <= 233472, "two CTAs to an SM");
 
 constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kH, kTile, false);
 
@@ -86,12 +87,13 @@ template <int kN>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory"); }
 
 template <int kStages>
-__global__ void __launch_bounds__(kThreads, kStages == kShortStages ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, kStages == kStagesTwo ? 2 : 1)
 score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
   using La = Layout<kStages>;
   constexpr int FULL = La::FULL, EMPTY = La::EMPTY, Q_FULL = La::Q_FULL, Q_EMPTY = La::Q_EMPTY, DONE = La::DONE;
   constexpr int kOffBar = La::kOffBar, kOffSlot = La::kOffSlot, kOffStats = La::kOffStats, kAhead = La::kAhead;
   constexpr int kTiles = La::kTmemCols / kTile;   // most tiles of a CTA
+  constexpr int kQSlots = La::kQSlots, kOffRing = La::kOffRing;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -192,36 +194,51 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
     const bool ok = __all_sync(0xffffffffu, gemm::wait(bar(DONE), 0, abort));
     ptx::tc_fence_after();
     const float s2 = p.scale_log2;
-    float m = -INFINITY, l = 0.f;
-    for (int t = 0; t < tiles && ok; ++t) {
-      const int valid = n - t * kTile;
-      const int c = half * (kTile / 2);
-      if (c >= valid) continue;
-      uint32_t r0v[32], r1v[32];
+    // the maximum first, so that the exponentials, which go back into the accumulator's place, share one
+    // reference and are never computed again (the exponential unit is what these passes are bound by)
+    auto load = [&](int t, uint32_t (&r0v)[32], uint32_t (&r1v)[32]) {   // 64 pages; those past the end at -inf
+      const int c = half * (kTile / 2), valid = n - t * kTile - c;
       ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c), r0v);
       ptx::tmem_ld32(tmem + lane_off + (uint32_t)(t * kTile + c + 32), r1v);
       ptx::tmem_wait_ld_regs(r0v);
       ptx::tmem_wait_ld_regs(r1v);
-      if (valid < c + 64) {   // pages past the end
+      if (valid < 64) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          if (c + j >= valid) r0v[j] = 0xff800000u;
-          if (c + 32 + j >= valid) r1v[j] = 0xff800000u;
+          if (j >= valid) r0v[j] = 0xff800000u;
+          if (32 + j >= valid) r1v[j] = 0xff800000u;
         }
       }
-      float mx[4] = {m, m, m, m}, sm[4] = {0.f, 0.f, 0.f, 0.f};
+    };
+    const int mine = ok ? max(0, (n - half * (kTile / 2) + kTile - 1) / kTile) : 0;   // tiles this half has pages of
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int t = 0; t < mine; ++t) {
+      uint32_t r0v[32], r1v[32];
+      load(t, r0v, r1v);
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         mx[j & 3] = fmaxf(mx[j & 3], fmaxf(__uint_as_float(r0v[j]), __uint_as_float(r1v[j])));
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), off = -mt * s2;
+    }
+    const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), off = -m * s2;
+#pragma unroll 1
+    for (int t = 0; t < mine; ++t) {
+      uint32_t r0v[32], r1v[32];
+      load(t, r0v, r1v);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        sm[j & 3] += ptx::ex2_approx(fmaf(__uint_as_float(r0v[j]), s2, off));
-        sm[(j + 2) & 3] += ptx::ex2_approx(fmaf(__uint_as_float(r1v[j]), s2, off));
+        const float e0 = ptx::ex2_approx(fmaf(__uint_as_float(r0v[j]), s2, off));
+        const float e1 = ptx::ex2_approx(fmaf(__uint_as_float(r1v[j]), s2, off));
+        sm[j & 3] += e0;
+        sm[(j + 2) & 3] += e1;
+        r0v[j] = __float_as_uint(e0);
+        r1v[j] = __float_as_uint(e1);
       }
-      l = l * ptx::ex2_approx((m - mt) * s2) + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
-      m = mt;
+      ptx::tmem_st32(tmem + lane_off + (uint32_t)(t * kTile + half * (kTile / 2)), r0v);
+      ptx::tmem_st32(tmem + lane_off + (uint32_t)(t * kTile + half * (kTile / 2) + 32), r1v);
     }
+    ptx::tmem_wait_st();
+    const float l = (sm[0] + sm[1]) + (sm[2] + sm[3]);
     __syncwarp();
     ptx::cluster_wait();
     for (int r = 0; r < csize; ++r) {
@@ -294,10 +311,13 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
       const float2 st = stats[r * kH + head];
       if (st.y != 0.f) l += st.y * ptx::ex2_approx((st.x - m) * s2);
     }
-    const float inv = head < p.H ? 1.f / l : 0.f, off = -m * s2;
-    // masses e^(u - m) / l, summed over the warp's 32 heads: at each step a lane keeps half of its columns and
+    // what this half's exponentials are to be multiplied by
+    const float own = stats[((int)rank * 2 + half) * kH + head].x;
+    const float f = head < p.H ? ptx::ex2_approx((own - m) * s2) / l : 0.f;
+    // masses, summed over the warp's 32 heads: at each step a lane keeps half of its columns and
     // adds the other lane's values of them, so that of 64 columns lane j ends with 2 j and 2 j + 1
     float* colsum = reinterpret_cast<float*>(gbase);   // [4][kMaxPages], over the query (its products are done)
+#pragma unroll 1
     for (int t = 0; t < tiles; ++t) {
       const int c = half * (kTile / 2);
       if (t * kTile + c >= n) break;
@@ -309,7 +329,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
       float a[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) {
-        const float e = ptx::ex2_approx(fmaf(__uint_as_float(j < 32 ? r0v[j & 31] : r1v[j & 31]), s2, off)) * inv;
+        const float e = __uint_as_float(j < 32 ? r0v[j & 31] : r1v[j & 31]) * f;
         a[j] = head < p.H ? e : 0.f;   // (rows past the last head may hold anything)
       }
 #pragma unroll
@@ -354,7 +374,7 @@ inline int resident_clusters(int c, int num_sms) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(num_sms / c * c));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<kLongStages>::kSmemBytes;
+  cfg.dynamicSmemBytes = Layout<kStagesOne>::kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
@@ -363,7 +383,7 @@ inline int resident_clusters(int c, int num_sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, score_kernel<kLongStages>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, score_kernel<kStagesOne>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = num_sms / c;
   }
@@ -378,10 +398,10 @@ inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const vo
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    if (cudaFuncSetAttribute(score_kernel<kLongStages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout<kLongStages>::kSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(score_kernel<kShortStages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout<kShortStages>::kSmemBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(score_kernel<kStagesOne>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<kStagesOne>::kSmemBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(score_kernel<kStagesTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<kStagesTwo>::kSmemBytes) != cudaSuccess)
       return MLA_ERR_CUDA;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
@@ -399,7 +419,7 @@ inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const vo
   cfg.gridDim = dim3((unsigned)(rows * c));
   cfg.blockDim = dim3(kThreads);
   const bool many_short = rows > num_sms && max_pages <= kTile;
-  cfg.dynamicSmemBytes = many_short ? Layout<kShortStages>::kSmemBytes : Layout<kLongStages>::kSmemBytes;
+  cfg.dynamicSmemBytes = many_short ? Layout<kStagesTwo>::kSmemBytes : Layout<kStagesOne>::kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -410,7 +430,7 @@ inline int launch_score(const mla_dims_t* d, int32_t rows, int32_t s_q, const vo
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, many_short ? score_kernel<kShortStages> : score_kernel<kLongStages>, tm_q, prm);
+  cudaLaunchKernelEx(&cfg, many_short ? score_kernel<kStagesTwo> : score_kernel<kStagesOne>, tm_q, prm);
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
