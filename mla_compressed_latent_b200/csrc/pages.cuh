@@ -253,12 +253,15 @@ __global__ void __launch_bounds__(256) score_mass_kernel(ScoreArgs A) {
 // =============================================================================================
 // Selection: the k pages of largest score among those a token sees, as an ascending list. The first
 // n_first and the last n_recent visible pages are always in it; equal scores go to the lower page; a
-// NaN ranks below every number. One block per token. The k-th largest rank is found digit by digit
-// (four 8-bit digits of an order-preserving 32-bit rank, most significant first: a histogram of the
-// ranks that match the digits found so far, then the digit at which the count from above reaches k),
-// and one ordered pass writes the pages above it and the first of those equal to it. Counts are
-// integers, so the result does not depend on the order of the shared-memory additions. 64 tokens of 64
-// pages: 4.9 us; 512 tokens of up to 2048 pages: 11.7 us, a chain of four histograms and eight ordered steps.
+// NaN ranks below every number. One block per token. The rank of the last page taken is found digit by digit
+// (the 9, 8, 8 and 7 bits of an order-preserving 32-bit rank, most significant first: a histogram of the
+// ranks that match the digits found so far, then the digit at which the count from above reaches what
+// is left to take), and no further than to a digit all of whose ranks are taken: with scores that
+// differ two digits, the exponent and eight more bits, mostly are enough. One ordered pass then writes the
+// pages above it and the first of those equal to it. Counts are integers, so the result does not depend on the
+// order of the shared-memory additions. A chain of latencies: 64 tokens of 64 pages 3.4 us back to back; 512 tokens of
+// 2048 pages 11.0 us, 16 of 8192 10.8 us (13.2 and 23.3 us with four digits always and a block-wide step for every
+// 256 or 1024 pages).
 // =============================================================================================
 constexpr int kKeep = 8;   // ranks a thread holds in registers; a longer list is re-read
 
@@ -273,8 +276,10 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads)
 select_pages_kernel(const float* scores, int max_pages, const int32_t* seqlens, int s_q, int k,
                     int n_first, int n_recent, int32_t* list, int32_t* counts) {
-  __shared__ int hist[256];
-  __shared__ int s_digit, s_left;
+  constexpr int kBins = 512, kWarps = kThreads / 32, kEntries = kKeep * kWarps;
+  __shared__ int hist[kBins];
+  __shared__ int s_digit, s_left, s_all;
+  __shared__ int before[kEntries + 1];   // (above | equal << 16) of the warps' pages in order, then their sums
   __shared__ int warp_gt[32], warp_eq[32];
   grid_dependency_wait();
   allow_dependents();
@@ -293,35 +298,44 @@ select_pages_kernel(const float* scores, int max_pages, const int32_t* seqlens, 
     return;
   }
   const float* sc = scores + (int64_t)v * max_pages;
-  auto rank_at = [&](int p) -> uint32_t {
-    // the highest rank of a number is that of +inf: 0xff800000
-    return (p < n_first || p >= n - n_recent) ? 0xffffffffu : rank_of(sc[p]);
-  };
+  // bin b lies where the lane that sums bins b, b + 1, ... of a run of 16 reads without bank conflicts
+  constexpr int kPerLane = kBins / 32;
+  auto bin = [&](uint32_t b) { return (b % kPerLane) * 32 + b / kPerLane; };
+  const int groups = min(kKeep, (n + kThreads - 1) / kThreads);   // of the pages held in registers
+  // the pages always kept are not ranked (fewer than n, as k is)
+  auto forced = [&](int p) { return p < n_first || p >= n - n_recent; };
   uint32_t keep[kKeep];
 #pragma unroll
   for (int i = 0; i < kKeep; ++i) {
     const int p = i * kThreads + tid;
-    keep[i] = p < n ? rank_at(p) : 0u;
+    keep[i] = p < n && !forced(p) ? rank_of(sc[p]) : 0u;
   }
-  uint32_t found = 0, mask = 0;   // the digits of the k-th largest rank so far
-  int left = kept;                // how many of the ranks that match them are still to be taken
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
+  uint32_t found = 0, mask = 0;              // the digits found so far
+  int left = kept - n_first - n_recent;      // how many of the ranks that match them are still to be taken
+  bool all = left == 0;                      // every rank >= found is taken (none: found is above every rank)
+  if (all) found = 0xffffffffu;
+  for (int shift = 23, width = 9; !all && shift >= 0;) {
+    const uint32_t digit = (1u << width) - 1u;
+    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i)
-      if (i * kThreads + tid < n && (keep[i] & mask) == found) atomicAdd(&hist[(keep[i] >> shift) & 255u], 1);
+    for (int i = 0; i < kKeep; ++i) {
+      if (i >= groups) break;
+      const int p = i * kThreads + tid;
+      if (p < n && !forced(p) && (keep[i] & mask) == found) atomicAdd(&hist[bin((keep[i] >> shift) & digit)], 1);
+    }
     for (int p = kKeep * kThreads + tid; p < n; p += kThreads) {
-      const uint32_t r = rank_at(p);
-      if ((r & mask) == found) atomicAdd(&hist[(r >> shift) & 255u], 1);
+      if (forced(p)) continue;
+      const uint32_t r = rank_of(sc[p]);
+      if ((r & mask) == found) atomicAdd(&hist[bin((r >> shift) & digit)], 1);
     }
     __syncthreads();
     if (warp == 0) {
-      // lane l holds digits 255 - 8 l downwards: ranks with a digit at or above each
-      int c[8], sum = 0;
+      // lane l holds digits 511 - 16 l downwards: ranks with a digit at or above each
+      int c[kPerLane], sum = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        c[j] = hist[255 - 8 * lane - j];
+      for (int j = 0; j < kPerLane; ++j) {
+        c[j] = hist[bin(kBins - 1 - kPerLane * lane - j)];
         sum += c[j];
       }
       int above = sum;
@@ -332,46 +346,91 @@ select_pages_kernel(const float* scores, int max_pages, const int32_t* seqlens, 
       }
       above -= sum;   // in the lanes before this one
       if (above < left && left <= above + sum) {
-        int d = 0, a = above;
+        int d = 0, a = above, at = c[0];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (a + c[j] < left && d == j) { a += c[j]; d = j + 1; }
-        s_digit = 255 - 8 * lane - d;
+        for (int j = 0; j < kPerLane; ++j)
+          if (d == j) {
+            at = c[j];
+            if (a + c[j] < left) { a += c[j]; d = j + 1; }
+          }
+        s_digit = kBins - 1 - kPerLane * lane - d;
         s_left = left - a;
+        s_all = left - a == at;
       }
     }
     __syncthreads();
     found |= (uint32_t)s_digit << shift;
-    mask |= 255u << shift;
+    mask |= digit << shift;
     left = s_left;
+    all = s_all != 0;
+    width = shift >= 15 ? 8 : 7;
+    shift = shift == 23 ? 15 : shift == 15 ? 7 : shift == 7 ? 0 : -1;
   }
-  // ordered pass: page p goes to (pages above it so far) + (equal ones so far, `left` of them at most)
-  int gt0 = 0, eq0 = 0;
-  for (int base = 0, i = 0; base < n; base += kThreads, ++i) {
-    const int p = base + tid;
-    uint32_t r = 0;
-    if (i < kKeep) {
+  // in order: page p goes to (pages above found so far) + (equal ones so far, `left` of them at most)
+  auto above = [&](int p, uint32_t r) { return p < n && (forced(p) || (all ? r >= found && left > 0 : r > found)); };
+  auto equal = [&](int p, uint32_t r) { return p < n && !all && !forced(p) && r == found; };
+  auto place = [&](int p, bool gt, bool eq, uint32_t mg, uint32_t me, int g, int e) {
+    g += __popc(mg & ((1u << lane) - 1u));
+    e += __popc(me & ((1u << lane) - 1u));
+    if (gt || (eq && e < left)) out[g + min(e, all ? 0 : left)] = p;
+  };
 #pragma unroll
-      for (int j = 0; j < kKeep; ++j)
-        if (j == i) r = keep[j];
-    } else if (p < n) {
-      r = rank_at(p);
+  for (int i = 0; i < kKeep; ++i) {   // the pages held in registers: counts of every warp's 32 first
+    if (i >= groups) break;
+    const int p = i * kThreads + tid;
+    const uint32_t mg = __ballot_sync(0xffffffffu, above(p, keep[i])), me = __ballot_sync(0xffffffffu, equal(p, keep[i]));
+    if (lane == 0) before[i * kWarps + warp] = __popc(mg) | (__popc(me) << 16);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    constexpr int kPer = kEntries / 32;
+    int c[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      c[j] = kPer * lane + j < groups * kWarps ? before[kPer * lane + j] : 0;
+      sum += c[j];
     }
-    const bool gt = p < n && r > found, eq = p < n && r == found;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    int at = incl - sum;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      before[kPer * lane + j] = at;
+      at += c[j];
+    }
+    if (lane == 31) before[kEntries] = at;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    if (i >= groups) break;
+    const int p = i * kThreads + tid;
+    const bool gt = above(p, keep[i]), eq = equal(p, keep[i]);
+    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+    const int at = before[i * kWarps + warp];
+    place(p, gt, eq, mg, me, at & 0xffff, at >> 16);
+  }
+  int gt0 = before[kEntries] & 0xffff, eq0 = before[kEntries] >> 16;
+  for (int base = kKeep * kThreads; base < n; base += kThreads) {   // a longer list, 32 pages a warp at a time
+    const int p = base + tid;
+    const uint32_t r = p < n && !forced(p) ? rank_of(sc[p]) : 0u;
+    const bool gt = above(p, r), eq = equal(p, r);
     const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
     if (lane == 0) { warp_gt[warp] = __popc(mg); warp_eq[warp] = __popc(me); }
     __syncthreads();
     int g = gt0, e = eq0, tg = 0, te = 0;
 #pragma unroll 8
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       const int a = warp_gt[w], c = warp_eq[w];
       if (w < warp) { g += a; e += c; }
       tg += a;
       te += c;
     }
-    g += __popc(mg & ((1u << lane) - 1u));
-    e += __popc(me & ((1u << lane) - 1u));
-    if (gt || (eq && e < left)) out[g + min(e, left)] = p;
+    place(p, gt, eq, mg, me, g, e);
     gt0 += tg;
     eq0 += te;
     __syncthreads();

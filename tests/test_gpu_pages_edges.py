@@ -369,3 +369,21 @@ def test_append_fp8_of_more_tokens_than_one_wave():
     bar = np.maximum(2.0 ** -4 * np.abs(c), 2.0 ** -10 * got_s[:, None]) + 2 * slack * top[:, None]
     assert np.all(np.abs(F.e4m3_decode(codes.cpu().numpy()[at]) * got_s[:, None] - c) <= bar)
     assert np.all(np.abs(_f64(rope)[at] - kr) <= 2.0 ** -8 * np.abs(kr) + slack * max(1.0, np.abs(kr).max()))
+
+
+@pytest.mark.parametrize("n", [9, 300, 2048, 8200])
+@pytest.mark.parametrize("k,first,recent", [(3, 1, 2), (8, 8, 0), (7, 0, 3)])
+def test_select_when_forced_pages_fill_the_list_or_scores_differ_late(n, k, first, recent):
+    """Every place forced; scores equal in all but the last bits (the search runs to its last digit); a tie that
+    crosses the last place; nothing but NaN."""
+    g = torch.Generator().manual_seed(n + k)
+    late = (torch.full((n,), 0.37).view(torch.int32) + torch.randint(0, 3 * n, (n,), generator=g).int()).view(torch.float32)
+    tie = torch.full((n,), 2.0)
+    tie[torch.randperm(n, generator=g)[:k // 2]] = 5.0
+    x = torch.stack([late, tie, torch.full((n,), float("nan")), torch.randn(n, generator=g)])[:, None].contiguous()
+    lens = torch.full((4,), 64 * n, dtype=torch.int32, device="cuda")
+    pages, counts = ops.mla_select_pages(Dims(128, 128, 64, 512, 128), x.cuda(), lens, k, first, recent)
+    ok()
+    for b in range(4):
+        assert pages[b, 0].tolist() == PS.select(x[b, 0].tolist(), k, first, recent)
+    assert counts.flatten().tolist() == [k] * 4
