@@ -636,8 +636,9 @@ decode_simt_kernel(DecodeArgs A) {
     }
   }
 
-  const float inv_l = (l_run > 0.f) ? 1.f / l_run : 0.f;
-  const float lse = (l_run > 0.f) ? m_run + logf(l_run) : -INFINITY;
+  // no score above -inf: zeros and lse = -inf; a NaN sum goes on into both outputs
+  const float inv_l = l_run == 0.f ? 0.f : 1.f / l_run;
+  const float lse = l_run == 0.f ? -INFINITY : m_run + logf(l_run);
   if (A.nsplit == 1) {
     T* out = reinterpret_cast<T*>(A.out) + ((int64_t)tok * A.H + h) * A.out_head_stride;
 #pragma unroll
@@ -694,7 +695,7 @@ __global__ void merge_splits_kernel(const float* __restrict__ part_o, const floa
   for (int s = 0; s < nsplit; ++s) m = fmaxf(m, pl[s]);
   float tot = 0.f;
   for (int s = 0; s < nsplit; ++s) tot += (pl[s] == -INFINITY) ? 0.f : expf(pl[s] - m);
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;   // no visible position at all: zeros and lse = -inf
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;   // no visible position at all: zeros and lse = -inf (a NaN part stays NaN)
   for (int d = threadIdx.x; d < Dv; d += blockDim.x) {
     float acc = 0.f;
     for (int s = 0; s < nsplit; ++s) {
