@@ -331,6 +331,7 @@ __device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ len
     const int idx = q <= p1 ? slot(q) : -1;
     mx = fmaxf(mx, warp_max(idx >= 0 ? part_lse[(size_t)idx * kH + h] : -INFINITY));
   }
+  const float mref = mx == -INFINITY ? 0.f : mx;   // (every part empty: weights of 0)
   float tot = 0.f;
   float acc[16];
 #pragma unroll
@@ -339,8 +340,8 @@ __device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ len
   for (int q = p0; q <= p1; q += 2) {
     const int i0 = slot(q), i1 = q + 1 <= p1 ? slot(q + 1) : -1;
     float4 x0[4], x1[4];
-    const float w0 = i0 >= 0 ? exp2f((part_lse[(size_t)i0 * kH + h] - mx) * 1.4426950408889634f) : 0.f;
-    const float w1 = i1 >= 0 ? exp2f((part_lse[(size_t)i1 * kH + h] - mx) * 1.4426950408889634f) : 0.f;
+    const float w0 = i0 >= 0 ? exp2f((part_lse[(size_t)i0 * kH + h] - mref) * 1.4426950408889634f) : 0.f;
+    const float w1 = i1 >= 0 ? exp2f((part_lse[(size_t)i1 * kH + h] - mref) * 1.4426950408889634f) : 0.f;
     const float4* s0 = reinterpret_cast<const float4*>(part_o + ((size_t)max(i0, 0) * kH + h) * kDC) + lane;
     const float4* s1 = reinterpret_cast<const float4*>(part_o + ((size_t)max(i1, 0) * kH + h) * kDC) + lane;
 #pragma unroll
@@ -357,13 +358,13 @@ __device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ len
       acc[4 * k + 3] += w0 * x0[k].w + w1 * x1[k].w;
     }
   }
-  const float inv = 1.f / tot;
+  const float inv = tot != 0.f ? 1.f / tot : 0.f;
   uint2* dst = reinterpret_cast<uint2*>(o_lat + ((size_t)v * kH + h) * kDC) + lane;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     dst[32 * k] = make_uint2(ptx::pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
                              ptx::pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
-  if (lane == 0) lse[(size_t)v * kH + h] = mx + logf(tot);
+  if (lane == 0) lse[(size_t)v * kH + h] = tot != 0.f ? mref + logf(tot) : -INFINITY;
 }
 
 // The same for the sparse decode (one pair a part): one warp combines 128 of the 512 columns of row v and
@@ -814,18 +815,20 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
           }
           dec[row] = m_new;
           ptx::mbar_arrive(bar(DEC_FULL));
-          if (m_new != m_own) {   // this set's partial sum to the new maximum
-            l_own = (m_own == -INFINITY) ? 0.f : l_own * ptx::ex2_approx(m_own - m_new);
+          if (m_new != m_own) {   // this set's partial sum to the new maximum (before any: zero, or NaN)
+            if (m_own != -INFINITY) l_own *= ptx::ex2_approx(m_own - m_new);
             m_own = m_new;
           }
+          // while every score so far is -inf (or NaN) the exponents are taken against 0: weights of 0 (or NaN)
+          const float m_ref = m_new == -INFINITY ? 0.f : m_new;
           // exponentials, their sum, bf16 pairs
           uint32_t pk[32];
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 64; j += 2) {
             const bool in0 = valid >= kTile || j < valid, in1 = valid >= kTile || j + 1 < valid;
-            const float x0 = fmaf(__uint_as_float(v[j]), scale2, -m_new);
-            const float x1 = fmaf(__uint_as_float(v[j + 1]), scale2, -m_new);
+            const float x0 = fmaf(__uint_as_float(v[j]), scale2, -m_ref);
+            const float x1 = fmaf(__uint_as_float(v[j + 1]), scale2, -m_ref);
             const float e0 = in0 ? ptx::ex2_approx(x0) : 0.f;
             const float e1 = in1 ? ptx::ex2_approx(x1) : 0.f;
             ls[(j >> 1) & 3] += e0 + e1;
@@ -862,7 +865,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
           else if (wait_bar_warp(bar(DEC_FULL), last & 1u, abort_addr, true)) m_fin = dec[row];
           else ok = false;
         }
-        const float l_fin = (m_own == -INFINITY) ? 0.f : l_own * ptx::ex2_approx(m_own - m_fin);
+        const float l_fin = (m_own == -INFINITY) ? l_own : l_own * ptx::ex2_approx(m_own - m_fin);
         if (ptx::named_bar_or(2, kGroup, !ok)) { ok = false; break; }
         if (set == 1) dec[row] = l_fin;
         ptx::named_bar_sync(2, kGroup);
@@ -872,10 +875,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
           if (ok) {
             const bool partial = !(t_lo == 0 && t_hi == tiles_b);
             float* lse_dst = partial ? p.part_lse + ((size_t)pair * 2 + (seg > 0)) * kH : p.lse + (size_t)vrow(b) * kH;
-            // a segment with no visible position (a token's masked last tile alone) has l = 0:
-            // lse -inf and a zero part, which the merge weighs by 0
+            // a segment with no visible position (a token's masked last tile alone), or whose scores are
+            // all -inf, has l = 0: lse -inf and a zero part, which the merge weighs by 0. A NaN goes on
             lse_dst[row] = (m_fin + log2f(l)) * 0.69314718055994531f;
-            ptx::st_cluster_f32(stats_remote + row * 4u, l > 0.f ? 1.f / l : 0.f);
+            ptx::st_cluster_f32(stats_remote + row * 4u, l != 0.f ? 1.f / l : 0.f);
             ptx::mbar_arrive_remote(bar(STATS_FULL), 1);
           }
         }

@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 # one token whose list is cut over many workers, and many tokens whose lists are not
 CUT = {"dsv3_b64_l4096": [64 * 40 - 3], "smallem_fp32": [64 * 40]}
 WHOLE = {"dsv3_b64_l4096": [705 + 9 * i for i in range(70)], "smallem_fp32": [705 + i for i in range(300)]}
-FORMS = [("smallem_fp32", 16), ("smallem_fp32", 8)]
+FORMS = [("dsv3_b64_l4096", 16), ("smallem_fp32", 16), ("smallem_fp32", 8)]
 
 
 def _sparse(name, bits, lens, k, change):
@@ -117,7 +117,7 @@ def test_positions_with_scores_of_minus_infinity_weigh_nothing(name, bits, lens,
 
 
 @pytest.mark.parametrize("lens", [CUT, WHOLE], ids=["cut", "whole"])
-@pytest.mark.parametrize("name", ["smallem_fp32"])
+@pytest.mark.parametrize("name", ["dsv3_b64_l4096", "smallem_fp32"])
 def test_dense_decode_keeps_nan_too(name, lens):
     lens, head = lens[name], 3
     case = _case(name, lens)
