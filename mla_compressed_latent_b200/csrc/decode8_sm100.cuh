@@ -484,14 +484,16 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           }
           dec[row] = m_new;
           ptx::mbar_arrive(bar(DEC_FULL));
-          if (m_new != m_own) {
-            l_own = (m_own == -INFINITY) ? 0.f : l_own * ptx::ex2_approx(m_own - m_new);
+          if (m_new != m_own) {   // (before any score above -inf the sum is zero, or NaN)
+            if (m_own != -INFINITY) l_own *= ptx::ex2_approx(m_own - m_new);
             m_own = m_new;
           }
+          // while every score so far is -inf (or NaN) the exponents are taken against 0
+          const float m_ref = m_new == -INFINITY ? 0.f : m_new;
           // e, its sum, and w = e s, sixteen positions at a time
           uint32_t pk[32];
           uint64_t l2[2] = {0ull, 0ull};
-          const uint64_t scale22 = ptx::pack_f32x2(scale2, scale2), neg_m2 = ptx::pack_f32x2(-m_new, -m_new);
+          const uint64_t scale22 = ptx::pack_f32x2(scale2, scale2), neg_m2 = ptx::pack_f32x2(-m_ref, -m_ref);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint64_t e2[8], s2[8];
@@ -538,7 +540,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           else if (wait_bar_warp(bar(DEC_FULL), last & 1u, abort_addr, true)) m_fin = dec[row];
           else ok = false;
         }
-        const float l_fin = (m_own == -INFINITY) ? 0.f : l_own * ptx::ex2_approx(m_own - m_fin);
+        const float l_fin = (m_own == -INFINITY) ? l_own : l_own * ptx::ex2_approx(m_own - m_fin);
         if (ptx::named_bar_or(2, kGroup, !ok)) { ok = false; break; }
         if (set == 1) dec[row] = l_fin;
         ptx::named_bar_sync(2, kGroup);

@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 # one token whose list is cut over many workers, and many tokens whose lists are not
 CUT = {"dsv3_b64_l4096": [64 * 40 - 3], "smallem_fp32": [64 * 40]}
 WHOLE = {"dsv3_b64_l4096": [705 + 9 * i for i in range(70)], "smallem_fp32": [705 + i for i in range(300)]}
-FORMS = [("dsv3_b64_l4096", 16), ("smallem_fp32", 16), ("smallem_fp32", 8)]
+FORMS = [("dsv3_b64_l4096", 16), ("dsv3_b64_l4096", 8), ("smallem_fp32", 16), ("smallem_fp32", 8)]
 
 
 def _sparse(name, bits, lens, k, change):
