@@ -770,8 +770,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
     // launched cooperatively: when a row was cut, one grid-wide barrier, then the merge
     if (work[4] > 0 && work[5] == 0) {
       cooperative_groups::this_grid().sync();
-      sm100::merge_rows(p.counts, p.rows, p.k, sm100::active_groups<true>(npairs, work[4]), work[4], (int)blockIdx.x,
-                        (int)gridDim.x, kThreads / 32, p.part_o, p.part_lse, p.o_lat, p.lse);
+      sm100::merge_rows(p.counts, p.rows, p.k, sm100::active_groups<true>(npairs, work[4]), work[4],
+                        reinterpret_cast<sm100::CutRows*>(gbase), (int)blockIdx.x, (int)gridDim.x, kThreads / 32, p.part_o, p.part_lse, p.o_lat, p.lse);
     }
     allow_dependents();
   }

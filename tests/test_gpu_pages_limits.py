@@ -1,0 +1,89 @@
+"""The calls on 8-bit rows and on pages at the limits of what they take: thousands of uneven lists, scales
+of very different sizes in one tile, sequences that outgrow their table row, RoPE widths of any even size, calls of
+no rows, scores of -inf. Tolerances as in test_gpu_pages.py unless derived beside the test."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8_cache as F
+from oracle import page_select as PS
+from mla_compressed_latent_b200 import ops
+from mla_compressed_latent_b200.ops import Dims, LatentCache, LatentCacheFp8
+
+from _cases import TOL, TORCH_DT, max_rel_err
+from test_gpu_pages import HALF, _cache8, _cache16, _case, _f64, _lists, _rows, _score_case, ok
+
+pytestmark = pytest.mark.gpu
+
+DIMS = Dims(128, 128, 64, 512, 128)
+
+
+# ---- many uneven lists --------------------------------------------------------------------------------------
+
+
+def _ramp(n, bits):
+    """One sequence of n new tokens, each listing every page it sees: lists of 1 to n / 64 pages."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    P = n // 64
+    rows = torch.randn(P * 64, 576, device="cuda", generator=g).bfloat16()
+    q = (torch.randn(1, n, 128, 576, device="cuda", generator=g) * 0.4).bfloat16()
+    table = torch.randperm(P, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    counts = (torch.arange(n, device="cuda", dtype=torch.int32) // 64 + 1)[None]
+    pages = torch.arange(P, device="cuda", dtype=torch.int32).expand(1, n, P).contiguous()
+    pages[pages >= counts[..., None]] = -1
+    cache, held = LatentCache(rows[:, :512], rows[:, 512:], P), _f64(rows)
+    if bits == 8:
+        codes, scale = F.quantize_rows_f32(rows[:, :512].float().cpu().numpy())
+        cache = LatentCacheFp8(torch.from_numpy(codes).cuda(), torch.from_numpy(scale.astype(np.float32)).cuda(), rows[:, 512:], P)
+        held[:, :512] = F.dequantize_rows(codes, scale)
+    logical = held.reshape(P, 64, 576)[table[0].cpu().numpy()].reshape(-1, 576)
+    return q, cache, table, lens, pages, counts, logical
+
+
+def _time(call, n=5):
+    best = float("inf")
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_thousands_of_uneven_lists(bits):
+    """Joining the few rows that are cut must not add a step per pair of rows: the time is held to that of as many
+    tiles in lists of one length, which nothing is cut for (a scan of all rows by every row made it 9 times
+    that). The bar is 3.1: tiles are shared out evenly, 1824 to each of 73 pairs, and the pair at the start
+    of the ramp takes them in 448 rows of 1 to 7 pages, where an even list's takes 56 of 33; a row costs about 14 tiles beyond
+    its own, and (1824 + 448 * 14) / (56 * (33 + 14)) = 3.1."""
+    n = 4096
+    q, cache, table, lens, pages, counts, logical = _ramp(n, bits)
+    o = torch.empty(1, n, 128, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(1, n, 128, device="cuda")
+
+    def call():
+        ops.mla_decode_absorbed_sparse(DIMS, q, cache, table, lens, pages, counts, o, lse)
+
+    call()
+    ok()
+    for t in [0, 63, 64, 65, 1000, 2047, 2048, 3000, 3500, 3777, 3999, 4094, 4095] + list(range(2500, 2600, 7)):
+        ro, rl = PS.sparse_decode(_f64(q[0, t]), logical[:, :512], logical[:, 512:], np.arange(t // 64 + 1), t + 1, (128 + 64) ** -0.5)
+        assert max_rel_err(_f64(o[0, t]), ro) <= TOL["bf16"]["out"], t
+        assert np.abs(_f64(lse[0, t]) - rl).max() <= TOL["bf16"]["lse"], t
+    tiles = int(counts.sum())
+    long = _time(call)
+    even = torch.full_like(counts, tiles // n + 1)   # as many tiles in lists of one length, which nothing is cut for
+    even_pages = torch.arange(pages.shape[-1], device="cuda", dtype=torch.int32).expand_as(pages).contiguous()
+    even_lens = torch.tensor([n + 64 * pages.shape[-1]], dtype=torch.int32, device="cuda")   # (every token sees all of them)
+    big = torch.cat([table, table], 1)
+
+    def even_call():
+        ops.mla_decode_absorbed_sparse(DIMS, q, cache, big, even_lens, even_pages, even, o, lse)
+
+    even_call()
+    ok()
+    assert long <= 3.1 * _time(even_call)
