@@ -21,8 +21,10 @@
 // because only the former are scaled; the output CTA holds O in 512), eight row warps in two sets on
 // alternate tiles, P tiles handed over by bulk copies, lazy running maxima, ranges of tiles per pair and one
 // merge of cut rows. The reference M of a row's exponentials includes the scales: e = 2^(x - M) with
-// M >= max_j x_j + E - 14 and 2^E above the tile's scales, so that w = e s stays below 2^14; l sums the
-// same e, and O / l and M + log2 l need no correction.
+// M >= max_j (x_j + E_j) - 14 and 2^E_j above the scale of row j, so that w = e s stays below 2^14 and the
+// largest is 2^-3 or more: fp16 holds every weight that counts, whatever the scales are; l sums the same e, and
+// O / l and M + log2 l need no correction. Rows of one tile mostly have scales of a size (RMSNorm), and the
+// largest E then stands for all; a tile whose scales are further apart than 2^kNearLog2 takes each row's own.
 //
 // 64 rows of 40 pages (105 MB of codes, scales and keys, 46 GFLOP with the second term not counted): 67-70 us, where a
 // dequantising pass and the 16-bit decode took 124 us and attended rows rounded to bf16. A tile takes about
@@ -71,6 +73,12 @@ constexpr int kStgStride = kCopyBytes;
 constexpr int kSlotStride = 17408;                     // a multiple of 1024 (the swizzle repeat)
 // M moves when a tile would take a weight past 2^14; it then leaves room for 2^8 more
 constexpr float kTopLog2 = 14.0f, kRoomLog2 = 8.0f;
+constexpr int kNearLog2 = 8;
+// E at least this (a row of zeros has no E): e is at most 2^(14 - kMinLog2), so that a sum of 2^20 of them stays a
+// float. Scales lose bits of their weights only below 2^(kMinLog2 - 20).
+constexpr int kMinLog2 = -92;
+// 2^E is above the magnitude of a scale
+__device__ __forceinline__ int scale_log2(uint32_t bits) { return max((int)((bits >> 23) & 255u) - 126, kMinLog2); }
 
 constexpr int kOffK = 0;
 constexpr int kOffQR = kKStages * kKStageBytes;                       // the query's RoPE part, two boxes
@@ -422,7 +430,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
             ptx::fence_proxy_async_smem();
             __syncwarp();
           }
-          float smax = 0.f;
+          int e_top = kMinLog2, e_low = kMinLog2;
           uint64_t x2[32];   // x of positions 2 i, 2 i + 1
           const uint64_t unit2 = ptx::pack_f32x2(q_unit, q_unit);
           ptx::tc_fence_after();
@@ -432,9 +440,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
             ptx::tmem_ld32(tmem + lane_off + kSCol0 + 128u * sb + 32u * half, vc);
             ptx::tmem_ld32(tmem + lane_off + kSCol0 + 128u * sb + 64u + 32u * half, vr);
             if (half == 0) {
-              const float s0 = __uint_as_float(ptx::ld_shared_u32(sc_addr + 4u * lane));
-              const float s1 = __uint_as_float(ptx::ld_shared_u32(sc_addr + 4u * (lane + 32)));
-              smax = warp_max(fmaxf(fabsf(s0), fabsf(s1)));
+              const int e0 = scale_log2(ptx::ld_shared_u32(sc_addr + 4u * lane));
+              const int e1 = scale_log2(ptx::ld_shared_u32(sc_addr + 4u * (lane + 32)));
+              e_top = __reduce_max_sync(0xffffffffu, max(e0, e1));
+              // (slots past the end do not count)
+              e_low = __reduce_min_sync(0xffffffffu, min(lane < valid ? e0 : e_top, lane + 32 < valid ? e1 : e_top));
             }
             ptx::tmem_wait_ld_regs(vc);
             ptx::tmem_wait_ld_regs(vr);
@@ -461,17 +471,31 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
               x2[i] = ptx::pack_f32x2(2 * i < valid ? x0 : -INFINITY, 2 * i + 1 < valid ? x1 : -INFINITY);
             }
           }
-          // 2^E above every scale (E at least -100: smaller scales weigh nothing, and e stays finite)
-          const float e_tile = (float)max((int)(__float_as_uint(smax) >> 23) - 126, -100);
-          float a4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float x0, x1;
-            ptx::unpack_f32x2(x2[i], &x0, &x1);
-            a4[i & 3] = fmaxf(a4[i & 3], fmaxf(x0, x1));
-          }
           // the reference this tile needs: its weights below 2^kTopLog2
-          const float need = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3])) * scale2 + e_tile - kTopLog2;
+          float a4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, need;
+          if (e_top - e_low <= kNearLog2) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float x0, x1;
+              ptx::unpack_f32x2(x2[i], &x0, &x1);
+              a4[i & 3] = fmaxf(a4[i & 3], fmaxf(x0, x1));
+            }
+            need = fmaf(fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3])), scale2, (float)e_top - kTopLog2);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              uint64_t sc[2];
+              ptx::ld_shared_v2u64(sc_addr + 8u * i, &sc[0], &sc[1]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float x0, x1;
+                ptx::unpack_f32x2(x2[i + j], &x0, &x1);
+                a4[2 * j] = fmaxf(a4[2 * j], fmaf(x0, scale2, (float)scale_log2((uint32_t)sc[j])));
+                a4[2 * j + 1] = fmaxf(a4[2 * j + 1], fmaf(x1, scale2, (float)scale_log2((uint32_t)(sc[j] >> 32))));
+              }
+            }
+            need = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3])) - kTopLog2;
+          }
           float m_prev = -INFINITY;
           if (t > t_lo) {
             if (!wait_bar_warp(bar(DEC_FULL), (it - 1) & 1u, abort_addr, true)) { ok = false; continue; }

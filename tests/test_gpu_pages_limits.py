@@ -87,3 +87,46 @@ def test_thousands_of_uneven_lists(bits):
     even_call()
     ok()
     assert long <= 3.1 * _time(even_call)
+
+
+# ---- scales of one tile --------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("lens,k", [([64 * 9], 3), ([64 * 90], 40), ([64 * 6 + 3 + i for i in range(70)], 4)], ids=["one", "cut", "whole"])
+@pytest.mark.parametrize("size", [-8, -20, -26, -32, -60, -90])
+def test_a_small_row_that_takes_nearly_all_the_probability(lens, k, size):
+    """One row of a tile holds all but 2^-130 of every head's probability while its scale is 2^size of its
+    neighbours': the output is that row, however small."""
+    case = _case("dsv3_b64_l4096", lens)
+    w, dev = case.w, case.to_device()
+    cache, _ = _cache8(dev, case)
+    pages, counts = _lists(lens, 1, k, 3)
+    scales = cache.scales.cpu().numpy()
+    q = torch.zeros_like(case.q_abs)
+    q[..., :512] = case.q_abs[..., :512]
+    q[..., 512] = 8.0
+    pool = case.pool.clone()
+    pool[:, 512:] = 0
+    chosen = []
+    for b in range(w.B):
+        r = int(case.table[b, pages[b, 0, counts[b, 0] // 2]]) * 64 + (b * 11) % 64   # (a tile that is not the last)
+        chosen.append(r)
+        scales[r] = np.float32(2.0 ** size) * scales[r]
+        pool[r, 512] = 200.0   # q . k_r = 1600, times sm_scale = 1/sqrt(192): 115 above the others
+    dev["pool"][:, 512:] = pool[:, 512:].cuda()
+    cache.scales.copy_(torch.from_numpy(scales))
+    held = F.dequantize_rows(cache.codes.cpu().numpy(), scales)
+    case.pool, case.q_abs64 = pool, q.double().numpy()
+    o, lse = ops.mla_decode_absorbed_sparse(Dims.of(w), q.cuda(), cache, dev["table"], dev["seqlens"],
+                                            torch.from_numpy(pages).cuda(), torch.from_numpy(counts).cuda())
+    ok()
+    got, got_l = _f64(o)[:, 0], _f64(lse)[:, 0]
+    for b in {0, w.B // 2, w.B - 1}:
+        rows = _rows(case, b, held)
+        ro, rl = PS.sparse_decode(case.q_abs64[b, 0], rows[:, :512], rows[:, 512:], pages[b, 0, :counts[b, 0]], lens[b], w.sm_scale)
+        assert np.abs(ro - held[chosen[b]]).max() <= 1e-3 * np.abs(ro).max()   # (what the case is about)
+        assert max_rel_err(got[b], ro) <= TOL["bf16"]["out"], b
+        # lse: the bar and, as in the test of many sizes, what the query's second term may leave
+        mag = np.abs(case.q_abs64[b, 0])
+        terms = (mag @ np.abs(rows).T).max(1) * 576 * 2.0 ** -24 + mag.max(1) * 2.0 ** -18 * np.abs(rows).sum(1).max()
+        assert np.all(np.abs(got_l[b] - rl) <= 1e-3 + w.sm_scale * terms), b
