@@ -363,8 +363,9 @@ MLA_API int mla_read_latent_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B
  *     key_page = mean over the page's rows j below seqlens[b] of [c_j ; k_r,j]       (fp32 sums, one rounding)
  *   keys [num_pages, d_c + d_r] dtype, one row per pool page, row stride key_stride. s_q at least the
  *   longest sequence rebuilds every key. Other pages' keys are left as they were; a sequence of length
- *   0 writes nothing. Sequences may share pages that are full in each of them; the key of a page of which
- *   they hold different numbers of rows is undefined. The 8-bit form wants d_c a multiple of 16.
+ *   0 writes nothing. A sequence longer than its table row is reported (MLA_ERR_DEVICE_CHECK) whatever s_q is; keys
+ *   of its pages within the row are written. Sequences may share pages that are full in each of them; the key of a
+ *   page of which they hold different numbers of rows is undefined. The 8-bit form wants d_c a multiple of 16.
  * mla_score_pages: for each token (b, t), over the pages p that it sees (those with a position it sees),
  *     u_h,p = sm_scale * q_abs[b,t,h,:] · key_p          scores[b,t,p] = sum_h softmax_p(u_h)_p
  *   scores [B, s_q, max_pages] fp32; entries of pages the token does not see are left as they were. A

@@ -93,12 +93,10 @@ page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
   const int L = seqlens[b];
   if (L <= 0) return;
   const int page0 = max(0, L - s_q) / 64, last = (L - 1) / 64;
+  // a sequence longer than its table row is reported by its first block: the grid has none for pages past the row
+  if (i == 0 && last >= max_pages && threadIdx.x == 0) report(MLA_ERR_DEVICE_CHECK);
   const int p = page0 + i;
-  if (p > last) return;
-  if (p >= max_pages) {
-    if (threadIdx.x == 0) report(MLA_ERR_DEVICE_CHECK);
-    return;
-  }
+  if (p > last || p >= max_pages) return;
   const int page = block_table[(int64_t)b * max_pages + p];
   if (page < 0 || page >= cache.num_pages) {
     if (threadIdx.x == 0) report(MLA_ERR_DEVICE_CHECK);

@@ -130,3 +130,21 @@ def test_a_small_row_that_takes_nearly_all_the_probability(lens, k, size):
         mag = np.abs(case.q_abs64[b, 0])
         terms = (mag @ np.abs(rows).T).max(1) * 576 * 2.0 ** -24 + mag.max(1) * 2.0 ** -18 * np.abs(rows).sum(1).max()
         assert np.all(np.abs(got_l[b] - rl) <= 1e-3 + w.sm_scale * terms), b
+
+
+# ---- page keys ------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("s_q", [1, 64, 300, 100000])
+def test_page_keys_report_a_sequence_longer_than_its_table_row(bits, s_q):
+    case = _case("dsv3_b64_l4096", [256, 100])
+    w, dev = case.w, case.to_device()
+    cache = _cache8(dev, case)[0] if bits == 8 else _cache16(dev, case)
+    keys = torch.full((case.num_pages, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    table = dev["table"].contiguous()
+    lens = torch.tensor([64 * table.shape[1] + 1, 100], dtype=torch.int32, device="cuda")
+    ops.mla_update_page_keys(Dims.of(w), cache, table, lens, s_q, keys)
+    torch.cuda.synchronize()
+    assert ops.mla_check_status() == 6
+    assert bool((keys[int(case.table[1, 1])] != 7).any())   # the other sequence's key is written
