@@ -199,21 +199,23 @@ int launch_page_keys(const mla_dims_t* dims, int32_t B, int32_t s_q, const mla::
   // pages that s_q consecutive positions can touch, at most a whole table row
   const int per_seq = (int)std::min<int64_t>(max_pages, ((int64_t)s_q + 62) / 64 + 1);
   if ((int64_t)B * per_seq > INT32_MAX) return MLA_ERR_INVALID_ARG;
-  const size_t smem = (size_t)mla::pages::kKeyGroups * W * sizeof(float);
+  const size_t smem = (size_t)mla::pages::kKeyGroups * mla::pages::key_part_width(W) * sizeof(float);
   constexpr int V = mla::simt::Vec16<T>::n;
-  auto go = [&](auto kernel, int v) -> int {
+  auto go = [&](auto kernel, int v, int vr) -> int {
     if (int rc = set_smem(kernel, smem)) return rc;
-    const int threads = std::min(mla::pages::kKeyThreads, (W / v * mla::pages::kKeyGroups + 31) / 32 * 32);
+    const int pieces = dims->d_c / v + dims->d_r / vr;
+    const int threads = std::min(mla::pages::kKeyThreads, (pieces * mla::pages::kKeyGroups + 31) / 32 * 32);
     mla::launch_pdl(kernel, dim3(B * per_seq), dim3(threads), smem, st, view, block_table, max_pages, seqlens, s_q,
                     per_seq, dims->d_c, dims->d_r, (T*)keys, key_stride);
     return launch_status();
   };
   if constexpr (kCodes) {
-    if (dims->d_c % 16 || dims->d_r % V) return MLA_ERR_UNSUPPORTED;
-    return go(mla::pages::page_keys_kernel<T, V, true>, V);
+    if (dims->d_c % 16) return MLA_ERR_UNSUPPORTED;
+    if (dims->d_r % V) return go(mla::pages::page_keys_kernel<T, V, 1, true>, V, 1);
+    return go(mla::pages::page_keys_kernel<T, V, V, true>, V, V);
   } else {
-    if (dims->d_c % V == 0 && dims->d_r % V == 0) return go(mla::pages::page_keys_kernel<T, V, false>, V);
-    return go(mla::pages::page_keys_kernel<T, 1, false>, 1);
+    if (dims->d_c % V == 0 && dims->d_r % V == 0) return go(mla::pages::page_keys_kernel<T, V, V, false>, V, V);
+    return go(mla::pages::page_keys_kernel<T, 1, 1, false>, 1, 1);
   }
 }
 }  // namespace

@@ -78,15 +78,18 @@ __device__ __forceinline__ void add_raw_codes(const uint4& v, float sc, float (&
 }
 
 constexpr int kKeyGroups = 8;
+// floats from one group's sums to the next
+__host__ __device__ constexpr int key_part_width(int W) { return (W + 3) / 4 * 4; }
 constexpr int kKeyThreads = 640;   // most threads of a block
 
-// V: columns per piece (16 bytes of T, or 1 when a width is not a multiple of that); kCodes: 8-bit rows.
-template <typename T, int V, bool kCodes>
+// V, VR: columns per piece of the latent row (16 bytes of T, or 1 when a width is not a multiple of that) and of the
+// key; kCodes: 8-bit rows, whose latent width is a multiple of 16 and whose key may have any even one.
+template <typename T, int V, int VR, bool kCodes>
 __global__ void __launch_bounds__(kKeyThreads, 2)
 page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
                                  const int32_t* seqlens, int s_q, int per_seq, int d_c, int d_r,
                                  T* keys, int64_t key_stride) {
-  extern __shared__ __align__(16) float part[];   // [kKeyGroups][W]
+  extern __shared__ __align__(16) float part[];   // [kKeyGroups][WP]
   grid_dependency_wait();
   allow_dependents();
   const int b = blockIdx.x / per_seq, i = blockIdx.x % per_seq;
@@ -103,7 +106,7 @@ page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
     return;
   }
   const int n = min(64, L - p * 64);
-  const int W = d_c + d_r, Q = W / V, qc = d_c / V;
+  const int W = d_c + d_r, qc = d_c / V, Q = qc + d_r / VR, WP = key_part_width(W);
   for (int it = threadIdx.x; it < Q * kKeyGroups; it += blockDim.x) {
     const int q = it % Q, g = it / Q;
     float acc[V];
@@ -122,7 +125,7 @@ page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
         sc[u] = 0.f;
         if (r >= n) continue;
         if (q >= qc) {
-          raw[u] = load_raw<T, V>(cache.rope + row * cache.rope_stride + (q - qc) * V);
+          raw[u] = load_raw<T, VR>(cache.rope + row * cache.rope_stride + (q - qc) * VR);
         } else if constexpr (kCodes) {
           raw[u] = load_raw_codes<V>(cache.codes + row * cache.code_stride + q * V);
           sc[u] = cache.scales[row];
@@ -134,18 +137,20 @@ page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
       for (int u = 0; u < kBatch; ++u) {
         if constexpr (kCodes) {
           if (q < qc) add_raw_codes<V>(raw[u], sc[u], acc);
+          else if constexpr (VR == 1) acc[0] += __uint_as_float(raw[u].x);
           else add_raw<T, V>(raw[u], acc);
         } else {
           add_raw<T, V>(raw[u], acc);
         }
       }
     }
-    if constexpr (V == 1) {
-      part[g * W + q] = acc[0];
-    } else {   // (W is a multiple of V here: 16-byte stores)
+    float* dst = part + g * WP;
+    if (V == 1 || (VR == 1 && q >= qc)) {
+      dst[V == 1 ? q : d_c + (q - qc)] = acc[0];
+    } else {   // (16-byte stores: WP and, for VR = V, d_c are multiples of 4)
 #pragma unroll
-      for (int k = 0; k < V; k += 4)
-        *reinterpret_cast<float4*>(part + g * W + q * V + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+      for (int k = 0; k + 3 < V; k += 4)
+        *reinterpret_cast<float4*>(dst + q * V + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
     }
   }
   __syncthreads();
@@ -154,7 +159,7 @@ page_keys_kernel(CacheView<T> cache, const int32_t* block_table, int max_pages,
   for (int c = threadIdx.x; c < W; c += blockDim.x) {
     float s = 0.f;
 #pragma unroll
-    for (int g = 0; g < kKeyGroups; ++g) s += part[g * W + c];
+    for (int g = 0; g < kKeyGroups; ++g) s += part[g * WP + c];
     st(dst + c, s / fn);
   }
 }

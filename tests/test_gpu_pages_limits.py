@@ -148,3 +148,30 @@ def test_page_keys_report_a_sequence_longer_than_its_table_row(bits, s_q):
     torch.cuda.synchronize()
     assert ops.mla_check_status() == 6
     assert bool((keys[int(case.table[1, 1])] != 7).any())   # the other sequence's key is written
+
+
+@pytest.mark.parametrize("dtype,d_c,d_r", [("bf16", 64, 6), ("bf16", 512, 10), ("bf16", 16, 2), ("f32", 64, 6), ("f32", 128, 2),
+                                           ("bf16", 144, 12)])
+@pytest.mark.parametrize("lens,s_q", [([1], 1), ([63, 64, 65], 1), ([200, 1, 64], 66)])
+def test_page_keys_of_an_8_bit_cache_with_any_even_rope_width(dtype, d_c, d_r, lens, s_q):
+    case = _case("smallem_fp32", lens, dtype=dtype, d_c=d_c, d_r=d_r)
+    w, W = case.w, d_c + d_r
+    codes, scale = F.quantize_rows_f32(case.pool[:, :d_c].float().numpy())
+    rope = torch.full((case.num_pages * 64, (d_r + 7) // 8 * 8), float("nan"), dtype=case.pool.dtype)
+    rope[:, :d_r] = case.pool[:, d_c:]
+    cache = LatentCacheFp8(torch.from_numpy(codes).cuda(), torch.from_numpy(scale.astype(np.float32)).cuda(), rope.cuda()[:, :d_r],
+                           case.num_pages)
+    held = F.dequantize_rows(codes, scale)
+    keys = torch.full((case.num_pages, (W + 7) // 8 * 8), 7.0, dtype=TORCH_DT[dtype], device="cuda")
+    ops.mla_update_page_keys(Dims.of(w), cache, torch.from_numpy(case.table).cuda(), torch.from_numpy(case.lens).cuda(), s_q, keys[:, :W])
+    ok()
+    got, touched = _f64(keys[:, :W]), np.zeros(case.num_pages, bool)
+    for b, L in enumerate(lens):
+        rows = _rows(case, b, held)
+        ref = PS.page_keys(rows)
+        for p in range(max(0, L - s_q) // 64, (L - 1) // 64 + 1):
+            page = case.table[b, p]
+            touched[page] = True
+            mag = np.abs(rows[p * 64:p * 64 + 64]).mean(0)
+            assert np.all(np.abs(got[page] - ref[p]) <= HALF[dtype] * np.abs(ref[p]) + 66 * 2.0 ** -24 * mag)
+    assert np.all(got[~touched] == 7) and bool((keys[:, W:] == 7).all())
