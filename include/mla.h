@@ -339,7 +339,7 @@ MLA_API int mla_decode_absorbed_fp8(const mla_dims_t* dims, int32_t dtype, int32
  *   row_offsets[b + 1], holds position p = first[b] + r - row_offsets[b] of sequence b:
  *     out[r, 0:d_c] = s_p * value(code_p) (one rounding to dtype)     out[r, d_c:] = k_r,p
  *   first [B] int32 (NULL: all 0)   row_offsets [B + 1] int32, from 0, not falling   out [n_rows, d_c + d_r]
- *   dtype, row stride out_stride. Output rows from row_offsets[B] on are left as they were; offsets past
+ *   dtype, row stride out_stride; n_rows > 0. Output rows from row_offsets[B] on are left as they were; offsets past
  *   n_rows write nothing past it. A position outside the table row or a page id outside the pool is
  *   reported (MLA_ERR_DEVICE_CHECK) and its output row left as it was. d_c a multiple of 16.
  * ------------------------------------------------------------------------------------------- */

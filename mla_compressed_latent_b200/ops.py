@@ -412,7 +412,7 @@ def mla_append_cache_fp8(dims: Dims, x, w_dkv_kr, gamma, seqlens, block_table, c
 def mla_read_latent_fp8(dims: Dims, cache: LatentCacheFp8, block_table, row_offsets, out, first=None, stream=None):
     """Rows of an 8-bit cache back in storage type: out[row_offsets[b] + i] = [c ; k_r] of position
     first[b] + i (first None: from position 0) of sequence b. out [n_rows, d_c + d_r]; rows from
-    row_offsets[B] on are left as they were."""
+    row_offsets[B] on are left as they were. An out of no rows is a call without work."""
     lib = L.load()
     dt = _dt(out)
     dev = _current(out)
@@ -420,8 +420,10 @@ def mla_read_latent_fp8(dims: Dims, cache: LatentCacheFp8, block_table, row_offs
     table, max_pages, _ = _table(dev, B, block_table, None)
     off = _need(dev, "row_offsets", row_offsets, (B + 1,), torch.int32)
     pf = None if first is None else _need(dev, "first", first, (B,), torch.int32)
-    po, out_stride = _need_rows(dev, "out", out, 1, _width(dims), out.dtype)
+    po, out_stride = _need_rows(dev, "out", out, 0, _width(dims), out.dtype)
     cc = _cache_arg(dev, dims, cache, out.dtype)
+    if out.shape[0] == 0:   # a ragged batch without rows: nothing to enqueue (the library takes n_rows > 0)
+        return out
     d = dims.c()
     rc = lib.mla_read_latent_fp8(ctypes.byref(d), dt, B, ctypes.byref(cc), table, max_pages, pf, off, out.shape[0],
                                  po, out_stride, _stream_on(dev, stream))

@@ -175,3 +175,22 @@ def test_page_keys_of_an_8_bit_cache_with_any_even_rope_width(dtype, d_c, d_r, l
             mag = np.abs(rows[p * 64:p * 64 + 64]).mean(0)
             assert np.all(np.abs(got[page] - ref[p]) <= HALF[dtype] * np.abs(ref[p]) + 66 * 2.0 ** -24 * mag)
     assert np.all(got[~touched] == 7) and bool((keys[:, W:] == 7).all())
+
+
+# ---- read back ------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("name", ["dsv3_b64_l4096", "smallem_fp32"])
+def test_read_back_of_no_rows(name):
+    """A ragged batch in which no sequence has rows: nothing to do, and the arguments are checked all the same."""
+    case = _case(name, [70, 64])
+    w, dev = case.w, case.to_device()
+    cache, _ = _cache8(dev, case)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = torch.empty(0, w.d_c + w.d_r, dtype=TORCH_DT[w.dtype], device="cuda")
+    assert ops.mla_read_latent_fp8(Dims.of(w), cache, dev["table"], off, out) is out
+    ok()
+    with pytest.raises(ValueError):
+        ops.mla_read_latent_fp8(Dims.of(w), cache, dev["table"], off[:2], out)
+    with pytest.raises(ValueError):
+        ops.mla_read_latent_fp8(Dims.of(w), cache, dev["table"], off, out[:, 1:])
