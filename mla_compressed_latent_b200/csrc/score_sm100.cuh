@@ -220,7 +220,8 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
       for (int j = 0; j < 32; ++j)
         mx[j & 3] = fmaxf(mx[j & 3], fmaxf(__uint_as_float(r0v[j]), __uint_as_float(r1v[j])));
     }
-    const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), off = -m * s2;
+    // (nothing but -inf here: exponents against 0, so that they are masses of 0 and the sum is 0, or NaN)
+    const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), off = m == -INFINITY ? 0.f : -m * s2;
 #pragma unroll 1
     for (int t = 0; t < mine; ++t) {
       uint32_t r0v[32], r1v[32];

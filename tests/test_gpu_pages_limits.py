@@ -194,3 +194,31 @@ def test_read_back_of_no_rows(name):
         ops.mla_read_latent_fp8(Dims.of(w), cache, dev["table"], off[:2], out)
     with pytest.raises(ValueError):
         ops.mla_read_latent_fp8(Dims.of(w), cache, dev["table"], off, out[:, 1:])
+
+
+# ---- scores ---------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("name,lens,far", [
+    ("dsv3_b64_l4096", [64 * 65], [64]),                   # the only page of the second half of a tile
+    ("dsv3_b64_l4096", [64 * 100], list(range(64))),       # a whole half
+    ("dsv3_b64_l4096", [64 * 700], list(range(0, 128)) + [699]),
+    ("dsv3_b64_l4096", [64 * 700], list(range(600))),      # all pages of most of the cluster's CTAs
+    ("dsv3_b64_l4096", [64 * 65] + [64 * 3] * 200, [64]),  # two CTAs to an SM
+    ("smallem_fp32", [64 * 65], [64]),
+    ("dsv3_b64_l4096", [64 * 3, 64 * 9], [0, 2]),
+])
+def test_pages_whose_keys_score_minus_infinity_have_no_mass(name, lens, far):
+    w, table, num_pages, keys, q = _score_case(name, lens, 1, 3)
+    q[0, 0, :, 0] = q[0, 0, :, 0].abs().clamp_min(0.5)
+    keys[table[0, far].long(), 0] = float("-inf")
+    s = ops.mla_score_pages(Dims.of(w), q.cuda(), keys.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    ok()
+    n = lens[0] // 64
+    near = np.setdiff1d(np.arange(n), far)
+    k64, q64 = keys[table[0, near].long()].double().numpy(), q[0, 0].double().numpy()
+    ref = PS.page_scores(q64, k64, w.sm_scale)
+    got = _f64(s[0, 0])
+    eps = w.sm_scale * (w.d_c + w.d_r) * 2.0 ** -23 * (np.abs(q64) @ np.abs(k64).T).max()   # as in test_page_scores
+    assert np.all(got[far] == 0)
+    assert np.all(np.abs(got[near] - ref) <= (2 * eps + 2.0 ** -20) * ref)
