@@ -1,8 +1,4 @@
 // The 8-bit latent cache written straight from the projection, and read back into the storage type.
-//
-// (These kernels start while the kernel before them may still be writing their inputs, and wait for it. Their
-// pointers carry no restrict qualifier, so that no input is read through the non-coherent path, whose loads
-// nothing orders behind that wait.)
 #pragma once
 
 #include <cuda_fp16.h>

@@ -27,7 +27,9 @@ void launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaSt
 // Same, with programmatic dependent launch allowed: the kernel may be scheduled while the previous
 // kernel of the stream is still running, and runs its prologue (barrier setup, TMEM allocation) in
 // its shadow. Such a kernel calls grid_dependency_wait() before it touches global memory and
-// allow_dependents() once its own successor may be scheduled.
+// allow_dependents() once its own successor may be scheduled. Its inputs (and those of the device functions it
+// calls) carry no restrict qualifier: the kernel before it may write them while it runs, and a load through the
+// non-coherent path, which const with restrict allows, is ordered behind nothing.
 template <typename... KArgs, typename... Args>
 void launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};

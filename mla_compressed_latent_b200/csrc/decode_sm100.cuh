@@ -305,9 +305,9 @@ __device__ __forceinline__ int pair_of(long long x, long long T, int P) { return
 // One warp combines the parts of new token v (= b * s_q + tok) and head h, if its sequence was cut:
 // the parts come from pair (group, tok) of the groups that covered the sequence's tiles. T = total
 // tiles, G = groups; lane l holds sequences [b0, b1) for the prefix of tiles before b.
-__device__ __forceinline__ void merge_token_head(const int32_t* __restrict__ lens, int s_q, int max_tiles, int G,
+__device__ __forceinline__ void merge_token_head(const int32_t* lens, int s_q, int max_tiles, int G,
                                                  long long T, int b0, int b1, int v, int h,
-                                                 const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                                                 const float* part_o, const float* part_lse,
                                                  __nv_bfloat16* __restrict__ o_lat, float* __restrict__ lse) {
   const int lane = threadIdx.x & 31;
   const int b = v / s_q, tok = v % s_q;
@@ -428,7 +428,7 @@ __device__ __forceinline__ void find_cut_rows(const int32_t* counts, int rows, i
 // parts are found together, a part a lane, and the parts' values are loaded eight at a time: with few rows cut
 // over many pairs the merge is a chain of loads, and this makes it a short one.
 __device__ __forceinline__ void merge_row_quarter(const CutRow& c, int G, long long T, int h, int quarter,
-                                                  const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                                                  const float* part_o, const float* part_lse,
                                                   __nv_bfloat16* __restrict__ o_lat, float* __restrict__ lse) {
   const int lane = threadIdx.x & 31;
   const int v = c.row;
@@ -480,8 +480,8 @@ __device__ __forceinline__ void merge_row_quarter(const CutRow& c, int G, long l
 }
 // All cut rows: (row, head, quarter) units dealt out over the grid's warps, neighbours to different SMs.
 __device__ __forceinline__ void merge_rows(const int32_t* counts, int rows, int max_tiles, int G, long long T, CutRows* cut,
-                                           int block, int blocks, int warps, const float* __restrict__ part_o,
-                                           const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ o_lat,
+                                           int block, int blocks, int warps, const float* part_o,
+                                           const float* part_lse, __nv_bfloat16* __restrict__ o_lat,
                                            float* __restrict__ lse) {
   find_cut_rows(counts, rows, max_tiles, G, T, cut);
   const int units = cut->n * kH * 4;
@@ -1184,8 +1184,8 @@ constexpr int kMergeHeads = 4;
 constexpr int kMergeTokenBlocks = 8;   // blocks along the tokens; each strides over them
 template <bool kSparse>
 __global__ void __launch_bounds__(32 * kMergeHeads)
-merge_kernel(const int32_t* __restrict__ lens, int B, int s_q, int max_tiles, int npairs, const float* __restrict__ part_o,
-             const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ o_lat, float* __restrict__ lse) {
+merge_kernel(const int32_t* lens, int B, int s_q, int max_tiles, int npairs, const float* part_o,
+             const float* part_lse, __nv_bfloat16* __restrict__ o_lat, float* __restrict__ lse) {
   // blocks stride over the new tokens v = b * s_q + tok; a token's parts come from pair (group, tok) of
   // the groups that covered its sequence's tiles
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

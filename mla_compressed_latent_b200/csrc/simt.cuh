@@ -109,9 +109,9 @@ __host__ __device__ inline int finish_readers(int N, int groups) { return (group
 // First half of an append finish, for token blockIdx.x: z[0..N) = the sums over the K slices (shared
 // memory), its cache row (-1: none, reported) and position in *s_row and *s_pos, and with groups > 0
 // the rotation's cos, sin of pair i at [2i], [2i + 1] of the array it returns.
-__device__ __forceinline__ float* finish_gather(const float* __restrict__ part, int ksplit, int n_tok, int s_q, int N,
-                                                int d_r, float rope_base, const int32_t* __restrict__ seqlens,
-                                                const int32_t* __restrict__ block_table, int max_pages,
+__device__ __forceinline__ float* finish_gather(const float* part, int ksplit, int n_tok, int s_q, int N,
+                                                int d_r, float rope_base, const int32_t* seqlens,
+                                                const int32_t* block_table, int max_pages,
                                                 int num_pages, int groups, float* z, long long* s_row, int* s_pos) {
   const int tok = blockIdx.x;
   const int b = tok / s_q, t = tok % s_q;
@@ -193,10 +193,10 @@ __device__ __forceinline__ void finish_rope(const float* zr, int half, const flo
 }
 
 template <typename T>
-__global__ void append_finish_kernel(const float* __restrict__ part, int ksplit, int n_tok, int s_q,
-                                     int d_c, int d_r, const T* __restrict__ gamma, float eps,
-                                     float rope_base, const int32_t* __restrict__ seqlens,
-                                     const int32_t* __restrict__ block_table, int max_pages,
+__global__ void append_finish_kernel(const float* part, int ksplit, int n_tok, int s_q,
+                                     int d_c, int d_r, const T* gamma, float eps,
+                                     float rope_base, const int32_t* seqlens,
+                                     const int32_t* block_table, int max_pages,
                                      T* latent, int64_t lat_stride, T* rope, int64_t rope_stride,
                                      int num_pages, int latent_by_token, int groups) {
   extern __shared__ float z[];
@@ -237,8 +237,8 @@ __global__ void append_finish_kernel(const float* __restrict__ part, int ksplit,
 // time (row widths are multiples of 16 bytes). One block per new token.
 // =============================================================================================
 template <typename T>
-__global__ void gqa_scatter_kernel(const T* __restrict__ kbuf, const T* __restrict__ vbuf, int s_q, int kw, int vw,
-                                   const int32_t* __restrict__ seqlens, const int32_t* __restrict__ block_table,
+__global__ void gqa_scatter_kernel(const T* kbuf, const T* vbuf, int s_q, int kw, int vw,
+                                   const int32_t* seqlens, const int32_t* block_table,
                                    int max_pages, int num_pages, T* k, int64_t k_stride, T* v, int64_t v_stride) {
   grid_dependency_wait();
   allow_dependents();
@@ -265,7 +265,7 @@ __global__ void gqa_scatter_kernel(const T* __restrict__ kbuf, const T* __restri
 // Four columns per thread (M a multiple of 4), one block row of tokens per blockIdx.y.
 // =============================================================================================
 template <typename T>
-__global__ void reduce_slices_kernel(const float* __restrict__ part, int ksplit, int n_tok, int M, T* out,
+__global__ void reduce_slices_kernel(const float* part, int ksplit, int n_tok, int M, T* out,
                                      int64_t out_stride) {
   grid_dependency_wait();
   allow_dependents();
@@ -294,8 +294,8 @@ __global__ void reduce_slices_kernel(const float* __restrict__ part, int ksplit,
 constexpr int RMS_THREADS = 1024;
 
 template <typename T>
-__global__ void __launch_bounds__(RMS_THREADS) rms_rows_kernel(const float* __restrict__ part, int ksplit, int n_tok, int N,
-                                const T* __restrict__ gamma, float eps, T* __restrict__ out, int groups) {
+__global__ void __launch_bounds__(RMS_THREADS) rms_rows_kernel(const float* part, int ksplit, int n_tok, int N,
+                                const T* gamma, float eps, T* __restrict__ out, int groups) {
   extern __shared__ float z[];
   __shared__ float red[32];
   grid_dependency_wait();   // launched with programmatic dependent launch after the projection
@@ -455,9 +455,9 @@ __device__ __forceinline__ float e4m3_value(uint32_t c) {
 // A page id outside the pool is reported and its rows are zeros. d_c % 16 == 0, d_r % 8 == 0.
 // =============================================================================================
 __global__ void __launch_bounds__(256)
-dequant_pages_kernel(const uint8_t* __restrict__ codes, int64_t code_stride, const float* __restrict__ scales,
-                     const __nv_bfloat16* __restrict__ rope, int64_t rope_stride, int num_pages,
-                     const int32_t* __restrict__ seqlens, const int32_t* __restrict__ block_table, int max_pages,
+dequant_pages_kernel(const uint8_t* codes, int64_t code_stride, const float* scales,
+                     const __nv_bfloat16* rope, int64_t rope_stride, int num_pages,
+                     const int32_t* seqlens, const int32_t* block_table, int max_pages,
                      int d_c, int d_r, __nv_bfloat16* __restrict__ lat_out, __nv_bfloat16* __restrict__ rope_out,
                      int32_t* __restrict__ dense_table) {
   __shared__ float lut[256];
