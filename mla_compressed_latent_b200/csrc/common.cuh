@@ -56,6 +56,19 @@ __device__ int g_status;
 
 __device__ __forceinline__ void report(int code) { atomicCAS(&g_status, 0, code); }
 
+#ifdef MLA_TEST_HOOKS
+// Test builds only: makes a bounded wait inside a tensor-core kernel run out. Bits 0-7 choose who waits: 1 the issuer
+// of a projection's, the scores' or the decode's score products, 2 the issuer of the decode's output products; the
+// bits above give the step (chunk, stage or tile) before which it does. It waits, with a 10 ms limit, for a
+// barrier phase that only its own later commit completes, so that the path of a failed wait (status, abort, drain)
+// runs.
+__device__ int g_test_stall;
+constexpr uint64_t kTestStallNs = 10000000ull;
+__device__ __forceinline__ bool test_stall(int who, int step) {
+  return (g_test_stall & 255) == who && (g_test_stall >> 8) == step;
+}
+#endif
+
 // ---- storage types ---------------------------------------------------------------------------
 template <typename T> struct Store;
 template <> struct Store<float> {

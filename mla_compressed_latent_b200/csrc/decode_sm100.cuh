@@ -54,6 +54,7 @@ constexpr float kRescaleLog2 = 8.0f;                   // lazy rescale threshold
 constexpr int kThreads = 384;                          // 4 control warps + 8 row warps
 constexpr int kGroup = 256;                            // threads of the row warps (4-11)
 constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 50000000ull;             // for what was in flight when an abort was raised
 
 // Per-tile geometry of the row warps (4..11): warp w owns rows [32 q + 16 u, +16) with q = w % 4 (its
 // TMEM lane quarter, which only sub-partition q can reach) and u = (w - 4) / 4; lane t holds rows
@@ -98,7 +99,9 @@ enum Bar : int {
   Q_FULL = S_EMPTY + kSBufs, P_EMPTY = Q_FULL + 1, P_WRITTEN = P_EMPTY + kPSlots,
   STG_FREE = P_WRITTEN + kStaging, STATS_EMPTY = STG_FREE + kStaging,
   DEC_FULL = STATS_EMPTY + 1, V_FULL = DEC_FULL + 1, V_EMPTY = V_FULL + kVStages, P_FULL = V_EMPTY + kVStages,
-  P_LOCAL = P_FULL + kPSlots, STATS_FULL = P_LOCAL + kPSlots, NUM_BARS = STATS_FULL + 1
+  P_LOCAL = P_FULL + kPSlots, STATS_FULL = P_LOCAL + kPSlots,
+  MMA_END = STATS_FULL + 1,   // [2]: an issuer's last products are done (output CTA: one issuer, the first)
+  NUM_BARS = MMA_END + 2
 };
 constexpr int kOffTmemSlot = kOffBar + NUM_BARS * 8;
 constexpr int kOffAbort = kOffTmemSlot + 8;
@@ -497,19 +500,25 @@ __device__ __forceinline__ void raise_abort(uint32_t abort_addr) {
 }
 
 // Slow path of wait_bar: polls until the phase completes. Returns false (and makes both CTAs
-// abort) after kTimeoutNs, or at once when an abort was raised and `stop_on_abort` is set.
+// abort) after kTimeoutNs, or at once when an abort was raised and `stop_on_abort` is set. A wait that an abort
+// does not end (for copies and loads in flight) goes on for kDrainNs after it: they take microseconds, but a
+// phase that needs another role to go on never completes then.
 __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, uint32_t abort_addr, bool cluster_scope,
                                            bool stop_on_abort) {
   const volatile int* abort_flag = reinterpret_cast<const volatile int*>(__cvta_shared_to_generic(abort_addr));
-  uint64_t t0 = 0;
+  uint64_t t0 = 0, limit = kTimeoutNs;
   for (uint32_t n = 0;; ++n) {
     const bool ok = cluster_scope ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
     if (ok) return true;
     if ((n & 15u) == 15u) {
-      if (stop_on_abort && *abort_flag) return false;
       const uint64_t now = ptx::globaltimer();
+      if (limit == kTimeoutNs && *abort_flag) {
+        if (stop_on_abort) return false;
+        t0 = now;
+        limit = kDrainNs;
+      }
       if (t0 == 0) t0 = now;
-      else if (now - t0 > kTimeoutNs) {
+      else if (now - t0 > limit) {
         report(MLA_ERR_TIMEOUT);
         raise_abort(abort_addr);
         return false;
@@ -529,6 +538,27 @@ __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, uin
   const bool ok = wait_bar(bar, parity, abort_addr, cluster_scope);
   return __all_sync(0xffffffffu, ok);
 }
+
+// An issuer's end: every product it issued is done (they read shared and tensor memory, which the CTA gives up
+// when it leaves). Normally they are by then, or the epilogue waits for them; after an abort nothing else does.
+__device__ __forceinline__ void end_products(uint32_t bar, uint32_t abort_addr) {
+  __syncwarp();
+  if (ptx::elect_one()) ptx::mma_commit(bar);
+  __syncwarp();
+  wait_bar(bar, 0, abort_addr, false, false);
+  __syncwarp();
+}
+#ifdef MLA_TEST_HOOKS
+// Waits in vain (see g_test_stall) for an issuer's end; false, after raising the abort.
+__device__ __forceinline__ bool stall_products(uint32_t bar, uint32_t abort_addr) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, 0) && ptx::globaltimer() - t0 < kTestStallNs) {}
+  report(MLA_ERR_TIMEOUT);
+  raise_abort(abort_addr);
+  __syncwarp();
+  return false;
+}
+#endif
 
 // ---- the kernel ------------------------------------------------------------------------------------
 // Warp roles.  Score CTA: 0 TMA producer | 1 S-MMA issuer for even tiles, warp 2 for odd tiles (each
@@ -568,7 +598,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
     ptx::mbar_init(bar(DEC_FULL), kH);   // one set's 128 row threads, once per tile
     ptx::mbar_init(bar(STATS_EMPTY), kGroup);
     for (int i = 0; i < kVStages; ++i) { ptx::mbar_init(bar(V_FULL + i), 1); ptx::mbar_init(bar(V_EMPTY + i), 1); }
-    ptx::mbar_init(bar(STATS_FULL), kH);   // one arrival per row (set 0 of the score CTA)
+    ptx::mbar_init(bar(STATS_FULL), kH);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(bar(MMA_END + i), 1);   // one arrival per row (set 0 of the score CTA)
     *reinterpret_cast<volatile int*>(gbase + kOffAbort) = 0;
     ptx::fence_mbar_init();
   }
@@ -743,6 +774,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
           if ((it & 1u) != parity) continue;
           const uint32_t sb = it % kSBufs;
           const uint32_t g0 = gq;
+#ifdef MLA_TEST_HOOKS
+          if (test_stall(1, (int)it) && !(ok = stall_products(bar(MMA_END + parity), abort_addr))) break;
+#endif
           if (!(ok = wait_bar_warp(bar(S_EMPTY + sb), ((it / kSBufs) & 1u) ^ 1u, abort_addr, false))) break;
           const uint32_t d = tmem + kSCol0 + 64u * sb;
 #pragma unroll
@@ -767,6 +801,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
           }
         }
       }
+      end_products(bar(MMA_END + parity), abort_addr);
     } else if (warp >= 4) {
       // ---- row warps: two sets of four warps take alternate tiles (set = it % 2); in a set, thread =
       // one head row of its warp's TMEM lane quarter, the whole 64-position row of S in registers
@@ -781,13 +816,14 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
       float* dec = reinterpret_cast<float*>(gbase + kOffStats);   // [128]: m after the latest tile
       uint32_t it = 0, seg = 0, gq = 0;
       bool ok = true;
-      while (ok && segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
+      // (a warp that has given up goes on to the next place where all of them meet, so that none waits there for it)
+      while (segs.next(lens, p.B, p.max_tiles, b, t_lo, t_hi, tiles_b)) {
         const int L = vlen(b);
         // Q̃ of this sequence into TMEM columns [0, 288), from the 6 ring groups that carry it (every
         // S MMA of the previous segment is done: the row warps met after its last result). Set g
         // fills column blocks [5g, 5 + 4g) of 64 values (32 TMEM columns).
         {
-          bool qok = true;
+          bool qok = ok;
           for (int qg = 0; qg < kQGroups; ++qg)
             qok = qok && wait_bar_warp(bar(K_FULL + (gq + qg) % kRing), ((gq + qg) / kRing) & 1u, abort_addr, false);
           ok = ok && qok;   // after a failure every row warp still meets the others at the segment end
@@ -987,6 +1023,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
         const int L = vlen(b);
         for (int t = t_lo; t < t_hi; ++t, ++it) {
           const uint32_t slot = it % kPSlots, s = it % kVStages;
+#ifdef MLA_TEST_HOOKS
+          if (test_stall(2, (int)it) && !(ok = stall_products(bar(MMA_END), abort_addr))) break;
+#endif
           if (!(ok = wait_bar_warp(bar(P_LOCAL + slot), (it / kPSlots) & 1u, abort_addr, false))) break;
           if (!(ok = wait_bar_warp(bar(V_FULL + s), (it / kVStages) & 1u, abort_addr, false))) break;
           // a tile past the token's last visible position (the last page of a sequence, or with
@@ -1027,6 +1066,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
           __syncwarp();
         }
       }
+      end_products(bar(MMA_END), abort_addr);
     } else if (warp >= 4) {
       // ---- row warps: rescale of the warp's own 16 rows of O before a tile whose P was computed
       // against a larger maximum, and the segment epilogue

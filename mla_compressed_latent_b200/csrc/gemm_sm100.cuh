@@ -77,12 +77,6 @@ __host__ __device__ constexpr int smem_bytes(int tn, int stages, int msub = 1) {
   return 1024 + kBarBytes + stages * stage_bytes(tn, msub);
 }
 
-#ifdef MLA_TEST_HOOKS
-// Test builds only: with g_test_stall set, each CTA's MMA issuer first waits for a barrier phase that
-// nothing completes, with a 10 ms limit, so that the bounded-wait path (status, abort, drain) runs.
-__device__ int g_test_stall;
-#endif
-
 // Waits for the phase of `parity`. Gives up (false) after limit_ns, recording MLA_ERR_TIMEOUT, or as
 // soon as *abort is set (when abort is given).
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const volatile int* abort = nullptr,
@@ -205,7 +199,7 @@ __device__ __forceinline__ void head_gemm_body(const CUtensorMap& tm_w, const CU
     bool live = true;
 #ifdef MLA_TEST_HOOKS
     // phase 0 of `done` completes only through this warp's own commit below: nothing else can end the wait
-    if (g_test_stall) live = wait(done, 0u, nullptr, 10000000ull);
+    if (test_stall(1, 0)) live = wait(done, 0u, nullptr, kTestStallNs);
 #endif
     for (int i = 0; i < nk && live; ++i) {
       const int s = i % S;

@@ -238,10 +238,9 @@ const char* mla_status_string(int s) {
 uint64_t mla_launch_count(void) { return mla::g_launches.load(std::memory_order_relaxed); }
 
 #ifdef MLA_TEST_HOOKS
-// Test builds only (not declared in mla.h): makes every per-head GEMM's MMA issuer wait for a phase
-// that nothing completes, so that a test can watch a bounded wait run out on the GPU.
+// Test builds only (not declared in mla.h): see g_test_stall.
 MLA_API int mla_test_set_stall(int on) {
-  return cudaMemcpyToSymbol(mla::gemm::g_test_stall, &on, sizeof(int)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return cudaMemcpyToSymbol(mla::g_test_stall, &on, sizeof(int)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 // Test builds only: the decode goes as two launches (decode, then the merge kernel) while on is set.
 MLA_API int mla_test_set_two_launches(int on) {
