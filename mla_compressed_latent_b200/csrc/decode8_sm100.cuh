@@ -107,7 +107,8 @@ enum Bar : int {
   K_FULL = 0, K_EMPTY = K_FULL + kKStages, S_FULL = K_EMPTY + kKStages, S_EMPTY = S_FULL + kSBufs,
   Q_LOADED = S_EMPTY + kSBufs, Q_FULL, P_EMPTY, P_WRITTEN = P_EMPTY + kPSlots, STG_FREE = P_WRITTEN + kStaging,
   STATS_EMPTY = STG_FREE + kStaging, DEC_FULL, V_FULL, V_EMPTY = V_FULL + kVStages, P_FULL = V_EMPTY + kVStages,
-  P_LOCAL = P_FULL + kPSlots, STATS_FULL = P_LOCAL + kPSlots, NUM_BARS
+  P_LOCAL = P_FULL + kPSlots, STATS_FULL = P_LOCAL + kPSlots, MMA_END,   // [2], as in the 16-bit decode
+  NUM_BARS = MMA_END + 2
 };
 constexpr int kOffTmemSlot = kOffBar + NUM_BARS * 8;
 constexpr int kOffAbort = kOffTmemSlot + 8;
@@ -189,6 +190,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
     ptx::mbar_init(bar(STATS_EMPTY), kGroup);
     for (int i = 0; i < kVStages; ++i) { ptx::mbar_init(bar(V_FULL + i), kGroup); ptx::mbar_init(bar(V_EMPTY + i), 1); }
     ptx::mbar_init(bar(STATS_FULL), kH);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(bar(MMA_END + i), 1);
     *reinterpret_cast<volatile int*>(gbase + kOffAbort) = 0;
     ptx::fence_mbar_init();
   }
@@ -329,6 +331,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
         for (int t = t_lo; t < t_hi; ++t, ++it) {
           if ((it & 1u) != parity) continue;
           const uint32_t sb = it % kSBufs, s = it % kKStages;
+#ifdef MLA_TEST_HOOKS
+          if (test_stall(1, (int)it) && !(ok = sm100::stall_products(bar(MMA_END + parity), abort_addr))) break;
+#endif
           if (!(ok = wait_bar_warp(bar(S_EMPTY + sb), ((it / kSBufs) & 1u) ^ 1u, abort_addr, false))) break;
           if (!(ok = wait_bar_warp(bar(K_FULL + s), (it / kKStages) & 1u, abort_addr, false))) break;
           if (ptx::elect_one()) {
@@ -352,6 +357,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           __syncwarp();
         }
       }
+      sm100::end_products(bar(MMA_END + parity), abort_addr);
     } else if (warp >= 4) {
       // ---- row warps: thread = one head row; two sets of four warps on alternate tiles
       const int set = (warp - 4) >> 2;
@@ -362,12 +368,13 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
       const float scale2 = p.sm_scale_log2;
       uint32_t it = 0, seg = 0;
       bool ok = true;
-      while (ok && next()) {
+      // (a warp that has given up goes on to the next place where all of them meet, so that none waits there for it)
+      while (next()) {
         const int L = vlen(b);
         // ---- the row's query: q 2^t as two E4M3 terms into TMEM. Each set takes half of its columns; the
         // row's largest value comes from both
         float q_unit = 0.f;   // 2^-t
-        ok = wait_bar_warp(bar(Q_LOADED), seg & 1u, abort_addr, false);
+        ok = ok && wait_bar_warp(bar(Q_LOADED), seg & 1u, abort_addr, false);
         uint32_t* q_top = reinterpret_cast<uint32_t*>(gbase + kOffQTop);
         const int r = row & 63, rh = row >> 6;
         if (ok) {
@@ -627,6 +634,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           ptx::tc_fence_before();
           ptx::mbar_arrive(bar(P_LOCAL + slot));
           if (warp != 1) continue;
+#ifdef MLA_TEST_HOOKS
+          if (test_stall(2, (int)it) && !(ok = sm100::stall_products(bar(MMA_END), abort_addr))) break;
+#endif
           if (!(ok = wait_bar_warp(bar(V_FULL + s), (it / kVStages) & 1u, abort_addr, false))) break;
           if (!(ok = wait_bar_warp(bar(P_LOCAL + slot), (it / kPSlots) & 1u, abort_addr, false))) break;
           if (ptx::elect_one()) {
@@ -646,6 +656,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_consta
           __syncwarp();
         }
       }
+      if (warp == 1) sm100::end_products(bar(MMA_END), abort_addr);
     } else {
       // ---- row warps: each tile's codes widened to fp16 on their way into shared memory, and the segment
       // epilogue.

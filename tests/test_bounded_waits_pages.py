@@ -76,7 +76,7 @@ def _decode_call(lib, kind, lens, k):
 ROWS = {"cut": ([64 * 300], 280), "one page": ([40 + i % 90 for i in range(300)], 1), "some pages": ([500 + i for i in range(150)], 7)}
 
 
-@pytest.mark.parametrize("kind", ["dense", "16-bit"])
+@pytest.mark.parametrize("kind", ["dense", "16-bit", "8-bit"])
 @pytest.mark.parametrize("rows", list(ROWS))
 @pytest.mark.parametrize("which,step", [(1, 0), (2, 0), (1, 1), (2, 1), (2, 2)])
 def test_decode(kind, rows, which, step):
