@@ -65,7 +65,8 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 }
 
 // Bounded wait for a phase that arrivals from either CTA complete; false on expiry (recorded) or abort.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const volatile int* abort,
+                                     uint64_t limit_ns = gemm::kTimeoutNs) {
   uint64_t t0 = 0;
   for (uint32_t n = 0;; ++n) {
     if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
@@ -73,7 +74,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const volati
       if (abort && *abort) return false;
       const uint64_t now = ptx::globaltimer();
       if (t0 == 0) t0 = now;
-      else if (now - t0 > gemm::kTimeoutNs) { report(MLA_ERR_TIMEOUT); return false; }
+      else if (now - t0 > limit_ns) { report(MLA_ERR_TIMEOUT); return false; }
     }
   }
 }
@@ -95,6 +96,8 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
   const uint32_t full0 = base, empty0 = base + 8u * kStages, done = base + 16u * kStages, slot = done + 8u;
   const uint32_t abort_addr = done + 16u;
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + (abort_addr - base));
+  const uint32_t begun_addr = abort_addr + 4u;   // K chunks this CTA's producer has begun
+  volatile int* begun = reinterpret_cast<volatile int*>(gbase + (begun_addr - base));
   const uint32_t ring = base + kBarBytes;
 
   if (threadIdx.x == 0) {
@@ -102,6 +105,7 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
     for (int s = 0; s < kStages; ++s) { ptx::mbar_init(full0 + 8u * s, 1); ptx::mbar_init(empty0 + 8u * s, 1); }
     ptx::mbar_init(done, 1);
     *abort = 0;
+    *begun = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tm_w);
     ptx::prefetch_tmap(&tm_x);
@@ -126,6 +130,12 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
     tma_load_2d_pair(st, &tm_w, f0, (kc0 + i) * kBK, full_cta0 + 8u * s);
     tma_load_2d_pair(st + kABytes / 2, &tm_w, f0 + 64, (kc0 + i) * kBK, full_cta0 + 8u * s);
   };
+  auto load_tokens = [&](int i) {   // (tokens past n_tok read zeros)
+    const uint32_t s = (uint32_t)(i % kStages), st = ring + s * kStageBytes;
+    for (int nb = 0; nb < nblk; ++nb)
+      tma_load_2d_pair(st + kABytes + nb * kBBytes, &tm_x, (kc0 + i) * kBK,
+                       tok0 + nb * kBlockN + (int)rank * (kBlockN / 2), full_cta0 + 8u * s);
+  };
   // The first two stages' weights are not written by the kernel before this one (as in the projections for
   // fewer tokens); everything else waits for it.
   const int pre = min(nk, 2);
@@ -138,24 +148,22 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
     // ---- TMA producer
     int i = 0;
     for (; i < nk; ++i) {
-      const uint32_t s = (uint32_t)(i % kStages), st = ring + s * kStageBytes;
+      const uint32_t s = (uint32_t)(i % kStages);
       if (i >= pre) {
         if (!wait(empty0 + 8u * s, ((i / kStages) & 1u) ^ 1u, abort)) { give_up(); break; }
         begin_stage(i);
       }
-      for (int nb = 0; nb < nblk; ++nb)   // (tokens past n_tok read zeros)
-        tma_load_2d_pair(st + kABytes + nb * kBBytes, &tm_x, (kc0 + i) * kBK,
-                         tok0 + nb * kBlockN + (int)rank * (kBlockN / 2), full_cta0 + 8u * s);
+      load_tokens(i);
     }
-    // after a failure what was issued must still land before the CTAs may exit (otherwise every stage
-    // was waited for by the issuer)
-    if (rank == 0 && *abort)
-      for (int k = (i > kStages ? i - kStages : 0); k < i; ++k) wait(full0 + 8u * (k % kStages), (k / kStages) & 1u, nullptr);
+    *begun = i;
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- MMA issuer: four K = 16 steps a chunk and product, M = 256 (both CTAs' features), N = 256
     const uint32_t idesc = ptx::idesc_bf16_f32_ab(kPairM, kBlockN, true, false);
     bool live = true;
     for (int i = 0; i < nk && live; ++i) {
+#ifdef MLA_TEST_HOOKS
+      if (test_stall(1, i) && !(live = wait(done, 0, nullptr, kTestStallNs))) break;
+#endif
       const uint32_t s = (uint32_t)(i % kStages), st = ring + s * kStageBytes;
       if (!wait(full0 + 8u * s, (i / kStages) & 1u, abort)) { live = false; break; }
       ptx::tc_fence_after();
@@ -179,7 +187,7 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
   // of the ring (free: every product is done), stored as 16-byte pieces. Warps 4-7 take the first product's
   // tokens and warps 0-3 the second's; of a single product each set takes every other 32.
   {
-    const bool ok = __all_sync(0xffffffffu, wait(done, 0, nullptr));
+    const bool ok = __all_sync(0xffffffffu, wait(done, 0, nullptr) && !*abort);
     ptx::tc_fence_after();
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     uint8_t* tile = gbase + kBarBytes + warp * 4096;
@@ -209,9 +217,27 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant
   }
   ptx::tc_fence_before();
   __syncthreads();
-  ptx::cluster_sync();   // both CTAs have read their accumulators
+  ptx::cluster_sync();   // both CTAs have read their accumulators, and nobody issues any more
+  if (*abort) {   // (the same in both CTAs)
+    // After a failure what was issued must still land before the CTAs may exit (otherwise the issuer waited for every
+    // stage). A stage's barrier counts both CTAs' bytes and one producer may have begun up to kStages more chunks
+    // than the other: what one has begun the other completes (the stage is free in both), and CTA 0, whose barriers
+    // they are, waits for all of them.
+    if (threadIdx.x == 0) {
+      int other;
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(other) : "r"(ptx::map_to_cta(begun_addr, rank ^ 1u)) : "memory");
+      const int own = *begun, n = max(own, other);
+      for (int i = own; i < n; ++i) { begin_stage(i); load_tokens(i); }
+      if (rank == 0)
+        for (int k = max(0, n - kStages); k < n; ++k) wait(full0 + 8u * (k % kStages), (k / kStages) & 1u, nullptr);
+    }
+    __syncwarp();
+    ptx::cluster_sync();   // no load is in flight to either CTA
+  }
   if (warp == 2) {
+    wait(done, 0, nullptr);   // (the products are done, also where the epilogue gave up before the issuer ended them)
     ptx::tc_fence_after();
+    __syncwarp();
     tmem_dealloc2(tmem);
   }
   ptx::cluster_sync();

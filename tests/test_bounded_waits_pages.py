@@ -83,3 +83,29 @@ def test_decode(kind, rows, which, step):
     lib = _load_test_lib()
     call, outputs, keep = _decode_call(lib, kind, *ROWS[rows])
     _stalls_then_clean(lib, call, outputs, which, step)
+
+
+@pytest.mark.parametrize("n_tok,C,gamma", [(1000, 7168, True), (1300, 1216, False), (4096, 2048, False)])
+@pytest.mark.parametrize("step", [0, 1, 3, 5])
+def test_append_of_many_tokens(n_tok, C, gamma, step):
+    lib = _load_test_lib()
+    g = torch.Generator(device="cuda").manual_seed(n_tok)
+    x = torch.randn(1, n_tok, C, device="cuda", generator=g).bfloat16()
+    w = (torch.randn(C, 576, device="cuda", generator=g) * C ** -0.5).bfloat16()
+    gm = torch.rand(512, device="cuda", generator=g).bfloat16() if gamma else None
+    pages = n_tok // 64 + 1
+    table = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)[None].contiguous()
+    lens = torch.tensor([n_tok], dtype=torch.int32, device="cuda")
+    codes = torch.empty(pages * 64, 512, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(pages * 64, device="cuda")
+    rope = torch.empty(pages * 64, 64, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    d = Dims(128, 128, 64, 512, 128).c()
+    cc = L.MlaLatentCacheFp8(codes.data_ptr(), 512, scales.data_ptr(), rope.data_ptr(), 64, pages)
+
+    def call(stream):
+        return lib.mla_append_cache_fp8(ctypes.byref(d), L.MLA_BF16, 1, n_tok, x.data_ptr(), C, w.data_ptr(),
+                                        gm.data_ptr() if gamma else None, lens.data_ptr(), table.data_ptr(), pages,
+                                        ctypes.byref(cc), ws.data_ptr(), ws.numel(), stream)
+
+    _stalls_then_clean(lib, call, [codes, scales, rope], 1, step)
