@@ -265,6 +265,12 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
     bool live = true;
     for (int i = 0, kc = 0, tile = 0; i < total && live; ++i) {
       const int s = i % kStages, qs = kc % kQSlots;
+#ifdef MLA_TEST_HOOKS
+      if (test_stall(1, i)) {
+        live = __all_sync(0xffffffffu, gemm::wait(bar(DONE), 0, nullptr, kTestStallNs));
+        if (!live) break;
+      }
+#endif
       if (tile == 0) {
         if (loaded < chunks) {   // the next chunk into the slot whose products were issued a chunk ago
           live = __all_sync(0xffffffffu, gemm::wait(bar(Q_EMPTY + loaded % kQSlots), ((loaded / kQSlots) & 1u) ^ 1u, abort));
@@ -353,6 +359,8 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const Params p) {
   }
   __syncthreads();
   if (warp == 8) {
+    gemm::wait(bar(DONE), 0);   // (also where the workers gave up before the products were done)
+    __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, La::kTmemCols);
   }

@@ -109,3 +109,23 @@ def test_append_of_many_tokens(n_tok, C, gamma, step):
                                         ctypes.byref(cc), ws.data_ptr(), ws.numel(), stream)
 
     _stalls_then_clean(lib, call, [codes, scales, rope], 1, step)
+
+
+@pytest.mark.parametrize("lens", [[64 * 50] * 3, [64 * 700, 64 * 1100], [64 * 60] * 200], ids=["short", "long", "two CTAs an SM"])
+@pytest.mark.parametrize("step", [0, 1, 4, 8])
+def test_scores(lens, step):
+    lib = _load_test_lib()
+    g = torch.Generator(device="cuda").manual_seed(len(lens))
+    B, P = len(lens), max(lens) // 64
+    keys = torch.randn(5000, 576, device="cuda", generator=g).bfloat16()
+    q = torch.randn(B, 1, 128, 576, device="cuda", generator=g).bfloat16()
+    table = torch.randint(0, 5000, (B, P), device="cuda", generator=g).to(torch.int32)
+    seqlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    scores = torch.empty(B, 1, P, device="cuda")
+    d = Dims(128, 128, 64, 512, 128).c()
+
+    def call(stream):
+        return lib.mla_score_pages(ctypes.byref(d), L.MLA_BF16, B, 1, q.data_ptr(), keys.data_ptr(), 576, 5000, table.data_ptr(), P,
+                                   seqlens.data_ptr(), scores.data_ptr(), None, 0, stream)
+
+    _stalls_then_clean(lib, call, [scores], 1, step)
