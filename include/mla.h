@@ -15,7 +15,9 @@
  *  - Row-major layouts; shapes are written [outer, ..., inner]. Every tensor pointer must be
  *    16-byte aligned and every row stride a multiple of 16 bytes.
  *  - dtype is MLA_F32 or MLA_BF16; it is the storage type of the cache, weights, queries and
- *    outputs of that call. Accumulation, softmax and normalisation are fp32 in every kernel.
+ *    outputs of that call. Accumulation, softmax and normalisation are fp32 in every kernel. The bf16
+ *    tensor-core decodes multiply the rows by softmax weights that are rounded once for that product, to bf16
+ *    (to fp16 over 8-bit rows); the weights' sum, which the output is divided by, holds them unrounded.
  *  - B sequences with s_q new tokens each: B * s_q must not exceed INT32_MAX (else
  *    MLA_ERR_INVALID_ARG).
  *  - seqlens[b] counts the cached positions of sequence b INCLUDING this step's s_q new tokens;
@@ -366,6 +368,10 @@ MLA_API int mla_read_latent_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B
  *   0 writes nothing. A sequence longer than its table row is reported (MLA_ERR_DEVICE_CHECK) whatever s_q is; keys
  *   of its pages within the row are written. Sequences may share pages that are full in each of them; the key of a
  *   page of which they hold different numbers of rows is undefined. The 8-bit form wants d_c a multiple of 16.
+ *   With several new tokens the key of a page that they share holds the rows of all of them, the later ones too: the
+ *   attention over chosen pages is causal, but an earlier token's scores, and so its choice, depend on later tokens
+ *   of the same step (drafts that are rejected afterwards among them). Where that matters, take the tokens one by
+ *   one with the lengths of each (seqlens[b] - s_q + t + 1, s_q = 1): keys, scores, selection.
  * mla_score_pages: for each token (b, t), over the pages p that it sees (those with a position it sees),
  *     u_h,p = sm_scale * q_abs[b,t,h,:] · key_p          scores[b,t,p] = sum_h softmax_p(u_h)_p
  *   scores [B, s_q, max_pages] fp32; entries of pages the token does not see are left as they were. A
@@ -379,7 +385,8 @@ MLA_API int mla_read_latent_fp8(const mla_dims_t* dims, int32_t dtype, int32_t B
  *   mla_decode_absorbed_fp8): a3 + a4 over the visible positions of the listed pages only. pages
  *   [B, s_q, k] and counts [B, s_q] as mla_select_pages writes them; a list must be strictly ascending and
  *   name visible pages (else MLA_ERR_DEVICE_CHECK is recorded and that token's outputs are undefined);
- *   entries from counts on are not read. A token with count 0 gets o_lat = 0 and lse = -inf.
+ *   entries from counts on are not read. A token with count 0 gets o_lat = 0 and lse = -inf, as does a head whose
+ *   scores are all -inf; a NaN among a head's scores makes its o_lat and lse NaN.
  *   A list of all visible pages gives mla_decode_absorbed's result. workspace: at least
  *   mla_decode_sparse_workspace_size / mla_decode_sparse_fp8_workspace_size bytes.
  * Errors otherwise as in the calls above.

@@ -433,7 +433,9 @@ def mla_read_latent_fp8(dims: Dims, cache: LatentCacheFp8, block_table, row_offs
 
 def mla_update_page_keys(dims: Dims, cache, block_table, seqlens, s_q: int, keys, stream=None):
     """keys [num_pages, d_c + d_r]: the mean row of every page that holds one of a sequence's s_q newest
-    positions, from a LatentCache or a LatentCacheFp8. s_q >= the longest sequence rebuilds every key."""
+    positions, from a LatentCache or a LatentCacheFp8. s_q >= the longest sequence rebuilds every key. A key
+    holds all of a page's rows below seqlens: with several new tokens, scores of the earlier ones depend on the later
+    ones unless keys and scores are made token by token (s_q = 1, seqlens lowered to the token's own)."""
     lib = L.load()
     dt = _dt(keys)
     dev = _current(keys)

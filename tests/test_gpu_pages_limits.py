@@ -222,3 +222,52 @@ def test_pages_whose_keys_score_minus_infinity_have_no_mass(name, lens, far):
     eps = w.sm_scale * (w.d_c + w.d_r) * 2.0 ** -23 * (np.abs(q64) @ np.abs(k64).T).max()   # as in test_page_scores
     assert np.all(got[far] == 0)
     assert np.all(np.abs(got[near] - ref) <= (2 * eps + 2.0 ** -20) * ref)
+
+
+# ---- several new tokens ---------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("L", [64 * 20 + 2, 64 * 20 + 40])   # the new tokens lie across two pages, or in one
+def test_tokens_of_a_step_taken_one_by_one_choose_pages_without_the_later_ones(bits, L):
+    """A page's key holds every row below seqlens, rows of later tokens of the same step among them. With the lengths
+    lowered to each token's own, and its key brought up to date before its scores, a token chooses as if the
+    later ones were not there, whatever they are; taken together, the scores of a token that shares a page with
+    later ones change with them."""
+    s_q, k = 4, 5
+    case = _case("dsv3_b64_l4096", [L], s_q)
+    w, dims = case.w, Dims.of(case.w)
+    got = []
+    for later in (0, 1):   # the same step with other rows for its last two tokens
+        dev = case.to_device()
+        if later:
+            for p in (L - 2, L - 1):
+                dev["pool"][int(case.table[0, p // 64]) * 64 + p % 64] *= -3
+        cache = _cache16(dev, case)
+        if bits == 8:
+            codes, scale = F.quantize_rows_f32(dev["pool"][:, :512].float().cpu().numpy())
+            cache = LatentCacheFp8(torch.from_numpy(codes).cuda(), torch.from_numpy(scale.astype(np.float32)).cuda(),
+                                   dev["pool"][:, 512:], case.num_pages)
+        q = dev["q_abs"] * 4
+        keys = torch.zeros(case.num_pages, 576, dtype=torch.bfloat16, device="cuda")
+        lens = [torch.tensor([L - s_q + t + 1], dtype=torch.int32, device="cuda") for t in range(s_q)]
+        ops.mla_update_page_keys(dims, cache, dev["table"], lens[0], L, keys)
+        alone = []
+        for t in range(s_q):
+            ops.mla_update_page_keys(dims, cache, dev["table"], lens[t], 1, keys)
+            scores = ops.mla_score_pages(dims, q[:, t:t + 1].contiguous(), keys, dev["table"], lens[t])
+            alone.append((scores, *ops.mla_select_pages(dims, scores, lens[t], k)))
+        together = ops.mla_score_pages(dims, q, keys, dev["table"], dev["seqlens"])
+        ok()
+        ref = PS.page_keys(_rows(case, 0, None)) if not later and bits == 16 else None
+        if ref is not None:   # the keys of the whole step are what the call for all of its tokens leaves
+            whole = torch.zeros_like(keys)
+            ops.mla_update_page_keys(dims, cache, dev["table"], dev["seqlens"], L, whole)
+            ok()
+            assert torch.equal(keys, whole)
+        got.append((alone, together))
+    for t in range(s_q - 2):
+        for a, b in zip(got[0][0][t], got[1][0][t]):
+            assert torch.equal(a, b), t
+        shared = (L - s_q + t) // 64 == (L - 2) // 64   # its last page holds the later tokens' rows too
+        assert torch.equal(got[0][1][:, t], got[1][1][:, t]) != shared, t
