@@ -5,6 +5,7 @@ makes an issuer of products wait, with a 10 ms limit, for a barrier phase that o
 completes; here the step before which it does so is chosen too, so that loads, copies and products of
 earlier steps are in flight or done."""
 import ctypes
+import functools
 import time
 
 import numpy as np
@@ -50,7 +51,14 @@ def _stalls_then_clean(lib, call, outputs, which, step):
         assert torch.equal(a, b)
 
 
-def _decode_call(lib, kind, lens, k):
+# one row cut over many pairs; one page a row, several rows to a pair; some tiles a row, several rows to a pair
+ROWS = {"cut": ([64 * 300], 280), "one page": ([40 + i % 90 for i in range(300)], 1), "some pages": ([500 + i for i in range(150)], 7)}
+
+
+@functools.lru_cache(maxsize=9)
+def _decode_call(kind, rows):
+    """A decode of the test build, its outputs, and what it keeps alive."""
+    lib, (lens, k) = _load_test_lib(), ROWS[rows]
     case = _case("dsv3_b64_l4096", lens)
     w, dev = case.w, case.to_device()
     d = Dims.of(w).c()
@@ -72,16 +80,12 @@ def _decode_call(lib, kind, lens, k):
     return lambda stream: fn(*args, stream), [o, lse], keep
 
 
-# one row cut over many pairs; one page a row, several rows to a pair; some tiles a row, several rows to a pair
-ROWS = {"cut": ([64 * 300], 280), "one page": ([40 + i % 90 for i in range(300)], 1), "some pages": ([500 + i for i in range(150)], 7)}
-
-
 @pytest.mark.parametrize("kind", ["dense", "16-bit", "8-bit"])
 @pytest.mark.parametrize("rows", list(ROWS))
 @pytest.mark.parametrize("which,step", [(1, 0), (2, 0), (1, 1), (2, 1), (2, 2)])
 def test_decode(kind, rows, which, step):
     lib = _load_test_lib()
-    call, outputs, keep = _decode_call(lib, kind, *ROWS[rows])
+    call, outputs, _ = _decode_call(kind, rows)
     _stalls_then_clean(lib, call, outputs, which, step)
 
 

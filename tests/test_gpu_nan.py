@@ -1,6 +1,9 @@
 """NaN and infinite scores in the decodes. A head whose query, or any of whose scores, is NaN has NaN outputs and a
 NaN lse, however the work was split; a position whose score is -inf weighs nothing; and only a token
 without a score above -inf has zeros and lse = -inf. Tolerances as in test_gpu_pages.py."""
+import copy
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -20,12 +23,24 @@ WHOLE = {"dsv3_b64_l4096": [705 + 9 * i for i in range(70)], "smallem_fp32": [70
 FORMS = [("dsv3_b64_l4096", 16), ("dsv3_b64_l4096", 8), ("smallem_fp32", 16), ("smallem_fp32", 8)]
 
 
+@functools.lru_cache(maxsize=8)
+def _base(name, bits, lens):
+    """The case, its 8-bit cache on the device and the rows that holds."""
+    case = _case(name, list(lens))
+    return (case, *_cache8(case.to_device(), case)) if bits == 8 else (case, None, None)
+
+
 def _sparse(name, bits, lens, k, change):
-    """The decode of a case whose inputs `change(case, q, rows, pages)` altered first; q [B, H, W] and the pool's rows
-    [rows, W] are fp64 copies whose non-finite entries are then carried into the device tensors."""
-    case = _case(name, lens)
+    """The decode of a case whose queries [B, H, W] and pool rows [rows, W] `change(case, q, rows, pages)` altered on the
+    device first; the case that is returned holds them as altered."""
+    case, cache, held = _base(name, bits, tuple(lens))
+    case = copy.copy(case)
     w, dev = case.w, case.to_device()
-    cache, held = _cache8(dev, case) if bits == 8 else (_cache16(dev, case), None)
+    if bits == 8:
+        cache = copy.copy(cache)
+        cache.rope = dev["pool"][:, w.d_c:]
+    else:
+        cache = _cache16(dev, case)
     pages, counts = _lists(lens, 1, k, 7)
     q, rows = dev["q_abs"], dev["pool"]
     change(case, q[:, 0], rows, pages[:, 0])
@@ -120,7 +135,7 @@ def test_positions_with_scores_of_minus_infinity_weigh_nothing(name, bits, lens,
 @pytest.mark.parametrize("name", ["dsv3_b64_l4096", "smallem_fp32"])
 def test_dense_decode_keeps_nan_too(name, lens):
     lens, head = lens[name], 3
-    case = _case(name, lens)
+    case = _base(name, 16, tuple(lens))[0]
     w, dev = case.w, case.to_device()
     q = dev["q_abs"]
     q[0, 0, head, 1] = float("nan")
