@@ -81,7 +81,7 @@ def load_peaks():
 # DRAM traffic of one decode_kernel launch (dram__bytes_read.sum + dram__bytes_write.sum) from an
 # ncu capture at dsv3_b64_l4096; reported only while the kernel's sources are the ones it was taken
 # on (their hash), otherwise the roofline's traffic is null.
-DECODE_TRAFFIC = {"workload": "dsv3_b64_l4096", "bytes": 313_053_952 + 3_316_480, "sources_sha256_16": "fc2e0b3820b39222"}
+DECODE_TRAFFIC = {"workload": "dsv3_b64_l4096", "bytes": 312_981_760 + 3_151_872, "sources_sha256_16": "2a26e249599d533d"}
 DECODE_SOURCES = ("decode_sm100.cuh", "ptx_sm100.cuh", "common.cuh")
 # the same for one gqla_kernel launch at gqla_g8_b32_l8192
 GQLA_TRAFFIC = {"workload": "gqla_g8_b32_l8192", "bytes": 1_115_219_968 + 10_750_464, "sources_sha256_16": "f3c7b86a737c8ed9"}

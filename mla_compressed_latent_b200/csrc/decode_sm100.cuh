@@ -61,8 +61,8 @@ constexpr uint64_t kDrainNs = 50000000ull;             // for what was in flight
 // +t/4 and +t/4+8, columns 8j + 2 (t % 4) + {0, 1} (the tcgen05 16x256b shape). Two softmax warps per
 // sub-partition: one alone is bound by its own latency, two keep the exponential unit near its rate.
 // The weights e are rounded to bf16: both operands of the output product have one type, the rows' own. l sums them
-// unrounded. Of random rows the outputs are off by 0.0020 of their values where weights in fp32 leave 0.0017, nearly all
-// of both the final rounding.
+// unrounded. Of random rows the outputs are off by 0.0020 of their values, where weights in fp32 leave the 0.0017 of the
+// outputs' own rounding.
 constexpr int kPBytes = kH * kTile * 2;                // 16384: a P tile, bf16, K-major 128-byte swizzle
 // Rescale factors alpha: per row, 1 unless the row's running maximum moved at this tile.
 // staging buffer (score CTA) and P slot (output CTA) alike: P [128 rows] | alpha [128]
@@ -212,7 +212,8 @@ __host__ __device__ __forceinline__ int active_groups(int G, long long T) {
 // written and read again: about a tile's time for kPartsPerTile of them). So whole rows, dealt out
 // evenly, are taken unless their longest pair would work longer than all pairs on even shares of the
 // tiles. Measured, cut and whole: 124 rows of 4 pages 109 and 33 us, 16 of 16 47 and 32 us, 100 of 25 140
-// and 74 us, 48 of 44 (8-bit) 104 and 68 us; one row of 32 pages 25 us cut.
+// and 74 us, 48 of 44 (8-bit) 104 and 68 us; one row of 32 pages 25 us cut. (The 8-bit kernel goes by the same two
+// numbers; its tile takes 1.07 us and its start a little longer.)
 constexpr int kSegmentTiles = 14, kPartsPerTile = 4;
 template <bool kSparse>
 __host__ __device__ __forceinline__ bool nothing_cut(int B, int groups, long long T, int max_tb) {
@@ -601,8 +602,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant_
     ptx::mbar_init(bar(DEC_FULL), kH);   // one set's 128 row threads, once per tile
     ptx::mbar_init(bar(STATS_EMPTY), kGroup);
     for (int i = 0; i < kVStages; ++i) { ptx::mbar_init(bar(V_FULL + i), 1); ptx::mbar_init(bar(V_EMPTY + i), 1); }
-    ptx::mbar_init(bar(STATS_FULL), kH);
-    for (int i = 0; i < 2; ++i) ptx::mbar_init(bar(MMA_END + i), 1);   // one arrival per row (set 0 of the score CTA)
+    ptx::mbar_init(bar(STATS_FULL), kH);   // one arrival per row (set 0 of the score CTA)
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(bar(MMA_END + i), 1);
     *reinterpret_cast<volatile int*>(gbase + kOffAbort) = 0;
     ptx::fence_mbar_init();
   }
